@@ -348,6 +348,124 @@ size_t moe_w4_dense_mlp_workspace_bytes(int64_t T);
 int moe_w4_dense_mlp(const void *x, const void *w, int64_t T, void *y, void *workspace, size_t workspace_bytes,
                      void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of a block around the routed experts: products grouped by expert
+ * for bf16 / fp16 experts (forward and both gradients: the experts that the
+ * packer above takes in), products with 4-bit weight rows of any shape for a
+ * few tokens, and the norms before and after a block with its gate and
+ * residual scale.  Ownership, streams and errors are those of moe_w4_forward:
+ * the caller owns every buffer, work is enqueued on `stream` and the call
+ * returns without synchronising, arguments are checked before any HIP call,
+ * and only kernels are enqueued (no allocation, no memset), so the calls may be
+ * captured into a HIP graph.  They keep no state: calls on different streams
+ * are independent if they write different buffers (a workspace is written).
+ * ---------------------------------------------------------------------- */
+
+/* Element types. */
+#define MOE_W4_F32 0
+#define MOE_W4_BF16 1
+#define MOE_W4_F16 2
+
+/* Products grouped by expert with ragged row counts.  offsets: i32
+ * [n_groups + 1] on the device (the `offsets` region of a forward's workspace
+ * has this form); group e holds the rows offsets[e] <= r < offsets[e + 1]:
+ *   moe_w4_grouped_mm     y[r][n]     = sum_k x[r][k]  w[e][n][k]
+ *   moe_w4_grouped_mm_dx  dx[r][k]    = sum_n dy[r][n] w[e][n][k]
+ *   moe_w4_grouped_mm_dw  dw[e][n][k] = add[e][n][k] + sum_r dy[r][n] x[r][k]
+ * x, dx [M][K], y, dy [M][N], w [n_groups][N][K]: row-major elements of `dtype`
+ * (MOE_W4_BF16 or MOE_W4_F16); products are summed in fp32 and rounded once.
+ * dw and add: [n_groups][N][K] of dw_dtype (dtype or MOE_W4_F32); add may be
+ * NULL (then 0) or dw itself.  A group may be empty: its dw is add (or 0).
+ * Rows of y and dx before offsets[0] and from offsets[n_groups] on are not
+ * written, and no such row of x and dy reaches a result.
+ * Offsets ascend within [0, M].  They are read on the device only: values
+ * outside are taken as the nearest of [0, M], a group that would end before it
+ * begins is empty, and rows claimed by two groups hold either's result.
+ * The results of a call depend on its arguments only (no atomics).
+ * N, K: multiples of 8, 8 .. MOE_W4_GROUPED_MAX_DIM; M: 0 ..
+ * MOE_W4_GROUPED_MAX_ROWS; n_groups: 0 .. MOE_W4_GROUPED_MAX_GROUPS (0: nothing
+ * is written).  All pointers 16-byte aligned (offsets 4); an output overlaps
+ * no input (add == dw excepted).  EINVAL otherwise. */
+#define MOE_W4_GROUPED_MAX_GROUPS 1024
+#define MOE_W4_GROUPED_MAX_ROWS 1048576
+#define MOE_W4_GROUPED_MAX_DIM 32768
+int moe_w4_grouped_mm(const void *x, const void *w, const int32_t *offsets, int64_t n_groups, int64_t M, int64_t N,
+                      int64_t K, int dtype, void *y, void *stream);
+int moe_w4_grouped_mm_dx(const void *dy, const void *w, const int32_t *offsets, int64_t n_groups, int64_t M, int64_t N,
+                         int64_t K, int dtype, void *dx, void *stream);
+int moe_w4_grouped_mm_dw(const void *x, const void *dy, const int32_t *offsets, int64_t n_groups, int64_t M, int64_t N,
+                         int64_t K, int dtype, const void *add, void *dw, int dw_dtype, void *stream);
+
+/* Products of 4-bit weight rows with 1 .. MOE_W4_MATVEC_MAX_TOKENS tokens, the
+ * decode form of a linear in the experts' container format:
+ *   y[t][n] = sum_k code[n][k] scale[n][k / group] xr[t][k]
+ * with xr = x, or x with every 128-block rotated (H128) if `rotate` is not 0
+ * (for weights packed in the rotated basis, as moe_w4_pack_experts does).
+ * x: x_dtype (MOE_W4_BF16 or MOE_W4_F16) [M][K]; codes: u8 [N][K / 2], element k
+ * of a row in the low nibble of byte k / 2 when k is even, two's complement;
+ * scales: bf16 [N][K / group], group 32, 64 or 128; y: y_dtype (any) [M][N].
+ * Sums in fp32 (xr is held to 16 significant bits, or 24 when y is
+ * MOE_W4_F32), y rounded once.
+ * K: a multiple of 128 up to MOE_W4_MATVEC_MAX_K; N: 0 ..
+ * MOE_W4_MATVEC_MAX_N (0, or M == 0: nothing is enqueued).  workspace: at least
+ * moe_w4_matvec_workspace_bytes(M, K) bytes, contents on entry irrelevant.
+ * Pointers 16-byte aligned (scales 2); y overlaps no input and not the
+ * workspace.  EINVAL / EWORKSPACE otherwise. */
+#define MOE_W4_MATVEC_MAX_TOKENS 64
+#define MOE_W4_MATVEC_MAX_K 65536
+#define MOE_W4_MATVEC_MAX_N 16777216
+size_t moe_w4_matvec_workspace_bytes(int64_t M, int64_t K);   /* 0 for M or K out of range */
+int moe_w4_matvec(const void *x, const void *codes, const void *scales, int64_t M, int64_t N, int64_t K, int group,
+                  int rotate, int x_dtype, void *y, int y_dtype, void *workspace, size_t workspace_bytes,
+                  void *stream);
+
+/* The norms after and before a block, with the block's gate and the residual
+ * scale, in one pass over T rows of H elements (the stack's rmsnorm and residual
+ * add are the case without gain, gate and post-norm):
+ *   n  = y / sqrt(mean(y^2) + eps)      with MOE_W4_NORM_POST, else y
+ *   r' = resid + scale * gate * post_gain * n
+ *   x  = r' / sqrt(mean(r'^2) + eps) * pre_gain     with MOE_W4_NORM_PRE
+ * resid, resid_out: resid_dtype (dtype or MOE_W4_F32); y, x_out, gate and gains:
+ * dtype (any).  Everything is computed in fp32 and rounded once (x from the
+ * unrounded r').  gate: NULL (MOE_W4_GATE_NONE, taken as 1), [T] (one a token),
+ * [H] (one a channel) or [T][H].  post_gain, pre_gain: [H] or NULL (1; they
+ * need their norm's flag).  y NULL: x = norm(resid) alone (no gate, POST or
+ * resid_out then).  Without MOE_W4_NORM_PRE x_out is NULL.  resid_out may be
+ * resid itself.
+ * T: 0 .. MOE_W4_NORM_MAX_ROWS; H: a multiple of 8, 8 .. MOE_W4_NORM_MAX_WIDTH;
+ * eps >= 0, scale finite.  Pointers 16-byte aligned; outputs overlap nothing
+ * else.  EINVAL otherwise. */
+#define MOE_W4_NORM_POST 1
+#define MOE_W4_NORM_PRE 2
+#define MOE_W4_GATE_NONE 0
+#define MOE_W4_GATE_TOKEN 1
+#define MOE_W4_GATE_CHANNEL 2
+#define MOE_W4_GATE_FULL 3
+#define MOE_W4_NORM_MAX_ROWS 4194304
+#define MOE_W4_NORM_MAX_WIDTH 8192
+int moe_w4_norm_residual(const void *resid, const void *y, const void *gate, int gate_kind, float scale,
+                         const void *post_gain, const void *pre_gain, int flags, float eps, int64_t T, int64_t H,
+                         int dtype, int resid_dtype, void *resid_out, void *x_out, void *stream);
+
+/* Its backward pass.  resid_out: the r' that the forward pass wrote (resid for
+ * a call without y); y, gate, gains, scale, flags, eps: as in the forward pass.
+ * d_resid_out: the gradient of r' from the stream (resid_dtype), or NULL (0);
+ * d_x: the gradient of x (dtype; NULL without MOE_W4_NORM_PRE).  Writes
+ *   d_resid  [T][H] resid_dtype: the gradient of resid (may be d_resid_out itself)
+ *   d_y      [T][H] dtype (NULL without y)
+ *   d_gate   NULL, or fp32 [T], fp32 [H] or dtype [T][H], as gate's kind
+ *   d_post_gain, d_pre_gain   NULL, or fp32 [H], summed over the T rows
+ *            (zeros for T == 0), with their norm's flag only (a gain that is
+ *            NULL has a gradient too: that of a gain of 1).
+ * workspace: at least moe_w4_norm_workspace_bytes(T, H) bytes (partial sums).
+ * The sums' order depends on T and H only.  Checks and errors as above. */
+size_t moe_w4_norm_workspace_bytes(int64_t T, int64_t H);   /* 0 for T or H out of range */
+int moe_w4_norm_residual_backward(const void *resid_out, const void *y, const void *gate, int gate_kind, float scale,
+                                  const void *post_gain, const void *pre_gain, int flags, float eps, int64_t T,
+                                  int64_t H, int dtype, int resid_dtype, const void *d_resid_out, const void *d_x,
+                                  void *d_resid, void *d_y, void *d_gate, float *d_post_gain, float *d_pre_gain,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
 /* Static text for a status code. */
 const char *moe_w4_status_string(int status);
 

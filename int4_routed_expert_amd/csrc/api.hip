@@ -22,6 +22,13 @@ static_assert(MOE_W4_ROUTER_NORM_FLOOR == moe_w4::kNormFloor && MOE_W4_ROUTER_NO
                   MOE_W4_ROUTER_BIAS_SELECT_ONLY == moe_w4::kBiasSelectOnly,
               "router policy flags of the header and the kernels agree");
 
+static_assert(MOE_W4_F32 == moe_w4::kElemF32 && MOE_W4_BF16 == moe_w4::kElemBf16 && MOE_W4_F16 == moe_w4::kElemF16 &&
+                  MOE_W4_GATE_NONE == moe_w4::kGateNone && MOE_W4_GATE_TOKEN == moe_w4::kGateToken &&
+                  MOE_W4_GATE_CHANNEL == moe_w4::kGateChannel && MOE_W4_GATE_FULL == moe_w4::kGateFull &&
+                  MOE_W4_NORM_POST == moe_w4::kNormPost && MOE_W4_NORM_PRE == moe_w4::kNormPre &&
+                  MOE_W4_MATVEC_MAX_TOKENS == moe_w4::kMatvecMaxTokens,
+              "block operators: names of the header and the kernels agree");
+
 using namespace moe_w4;
 
 namespace {
@@ -472,6 +479,87 @@ StackWs stack_ws_parts(int64_t T) {
 }
 
 // ---------------------------------------------------------------------------
+// Checks of the block operators.
+// ---------------------------------------------------------------------------
+size_t elem_bytes(int dtype) { return dtype == MOE_W4_F32 ? 4 : 2; }
+bool is_elem(int dtype) { return dtype == MOE_W4_F32 || dtype == MOE_W4_BF16 || dtype == MOE_W4_F16; }
+bool is_elem16(int dtype) { return dtype == MOE_W4_BF16 || dtype == MOE_W4_F16; }
+
+// A buffer of a call (NULL: not given), its size and alignment.
+struct Span {
+    const void *p;
+    size_t bytes;
+    size_t align;
+};
+// Whether `out` (aligned, not NULL) overlaps none of the others.
+template <size_t N>
+bool apart(const Span &out, const Span (&others)[N]) {
+    for (const Span &o : others)
+        if (o.p && overlap(out.p, out.bytes, o.p, o.bytes)) return false;
+    return true;
+}
+
+bool grouped_sizes_ok(int64_t groups, int64_t M, int64_t N, int64_t K, int dtype) {
+    return groups >= 0 && groups <= MOE_W4_GROUPED_MAX_GROUPS && M >= 0 && M <= MOE_W4_GROUPED_MAX_ROWS && N >= 8 &&
+           N <= MOE_W4_GROUPED_MAX_DIM && N % 8 == 0 && K >= 8 && K <= MOE_W4_GROUPED_MAX_DIM && K % 8 == 0 &&
+           is_elem16(dtype);
+}
+
+// in: M x in_cols and w: groups x N x K -> out: M x out_cols
+int check_grouped_rows(const void *in, int64_t in_cols, const void *w, const int32_t *offsets, int64_t groups, int64_t M,
+                       int64_t N, int64_t K, const void *out, int64_t out_cols) {
+    if (!in || !w || !offsets || !out) return MOE_W4_EINVAL;
+    if (!aligned(in, MOE_W4_ALIGN) || !aligned(w, MOE_W4_ALIGN) || !aligned(out, MOE_W4_ALIGN) || !aligned(offsets, 4))
+        return MOE_W4_EINVAL;
+    const Span others[] = {{in, (size_t)(M * in_cols) * 2, 16}, {w, (size_t)(groups * N * K) * 2, 16},
+                           {offsets, (size_t)(groups + 1) * 4, 4}};
+    return apart({out, (size_t)(M * out_cols) * 2, 16}, others) ? MOE_W4_OK : MOE_W4_EINVAL;
+}
+
+size_t gate_elems(int kind, int64_t T, int64_t H) {
+    return kind == MOE_W4_GATE_TOKEN ? (size_t)T : kind == MOE_W4_GATE_CHANNEL ? (size_t)H
+           : kind == MOE_W4_GATE_FULL ? (size_t)(T * H) : 0;
+}
+
+bool norm_sizes_ok(int64_t T, int64_t H) {
+    return T >= 0 && T <= MOE_W4_NORM_MAX_ROWS && H >= 8 && H <= MOE_W4_NORM_MAX_WIDTH && H % 8 == 0;
+}
+
+// What the two passes check alike: sizes, types, flags and which inputs go together.
+bool norm_form_ok(const void *y, const void *gate, int gate_kind, float scale, const void *post_gain, const void *pre_gain,
+                  int flags, float eps, int64_t T, int64_t H, int dtype, int resid_dtype) {
+    if (!norm_sizes_ok(T, H) || !is_elem(dtype) || (resid_dtype != dtype && resid_dtype != MOE_W4_F32)) return false;
+    if ((flags & ~(MOE_W4_NORM_POST | MOE_W4_NORM_PRE)) != 0 || gate_kind < MOE_W4_GATE_NONE ||
+        gate_kind > MOE_W4_GATE_FULL)
+        return false;
+    if (!(eps >= 0.0f) || !isfinite(eps) || !isfinite(scale)) return false;
+    if ((post_gain && !(flags & MOE_W4_NORM_POST)) || (pre_gain && !(flags & MOE_W4_NORM_PRE))) return false;
+    if (T > 0 && (gate != nullptr) != (gate_kind != MOE_W4_GATE_NONE)) return false;
+    if (T > 0 && !y && (gate_kind != MOE_W4_GATE_NONE || (flags & MOE_W4_NORM_POST) || !(flags & MOE_W4_NORM_PRE)))
+        return false;
+    return true;
+}
+
+template <size_t N>
+bool all_aligned(const Span (&s)[N]) {
+    for (const Span &v : s)
+        if (v.p && !aligned(v.p, v.align)) return false;
+    return true;
+}
+
+// Every output (not NULL) apart from every input and from every other output.
+template <size_t NI, size_t NO>
+bool outputs_apart(const Span (&in)[NI], const Span (&out)[NO]) {
+    for (size_t i = 0; i < NO; ++i) {
+        if (!out[i].p) continue;
+        if (!apart(out[i], in)) return false;
+        for (size_t j = i + 1; j < NO; ++j)
+            if (out[j].p && overlap(out[i].p, out[i].bytes, out[j].p, out[j].bytes)) return false;
+    }
+    return true;
+}
+
+// ---------------------------------------------------------------------------
 // The forward without allocation (moe_w4_forward_static): its workspace is
 // this file-scope device array, one copy per GPU, held until the process
 // ends.  The array's name in host code is only a handle for the runtime; the
@@ -745,6 +833,127 @@ int moe_w4_generate_normal_bf16(uint64_t seed, uint32_t tensor_id, int64_t n, do
     (void)hipGetLastError();
     const uint64_t key = host_mix64(seed * 0x9E3779B97F4A7C15ull + (uint64_t)tensor_id);
     launch_gen_normal_bf16(key, n, normal_mult(sigma), 0, static_cast<uint16_t *>(out), static_cast<hipStream_t>(stream));
+    return device_status(hipGetLastError());
+}
+
+int moe_w4_grouped_mm(const void *x, const void *w, const int32_t *offsets, int64_t n_groups, int64_t M, int64_t N,
+                      int64_t K, int dtype, void *y, void *stream) {
+    if (!grouped_sizes_ok(n_groups, M, N, K, dtype)) return MOE_W4_EINVAL;
+    if (n_groups == 0 || M == 0) return MOE_W4_OK;
+    const int rc = check_grouped_rows(x, K, w, offsets, n_groups, M, N, K, y, N);
+    if (rc != MOE_W4_OK) return rc;
+    (void)hipGetLastError();
+    launch_grouped_mm(x, w, offsets, (int)n_groups, (int)M, (int)N, (int)K, dtype == MOE_W4_BF16, y,
+                      static_cast<hipStream_t>(stream));
+    return device_status(hipGetLastError());
+}
+
+int moe_w4_grouped_mm_dx(const void *dy, const void *w, const int32_t *offsets, int64_t n_groups, int64_t M, int64_t N,
+                         int64_t K, int dtype, void *dx, void *stream) {
+    if (!grouped_sizes_ok(n_groups, M, N, K, dtype)) return MOE_W4_EINVAL;
+    if (n_groups == 0 || M == 0) return MOE_W4_OK;
+    const int rc = check_grouped_rows(dy, N, w, offsets, n_groups, M, N, K, dx, K);
+    if (rc != MOE_W4_OK) return rc;
+    (void)hipGetLastError();
+    launch_grouped_mm_dx(dy, w, offsets, (int)n_groups, (int)M, (int)N, (int)K, dtype == MOE_W4_BF16, dx,
+                         static_cast<hipStream_t>(stream));
+    return device_status(hipGetLastError());
+}
+
+int moe_w4_grouped_mm_dw(const void *x, const void *dy, const int32_t *offsets, int64_t n_groups, int64_t M, int64_t N,
+                         int64_t K, int dtype, const void *add, void *dw, int dw_dtype, void *stream) {
+    if (!grouped_sizes_ok(n_groups, M, N, K, dtype) || (dw_dtype != dtype && dw_dtype != MOE_W4_F32)) return MOE_W4_EINVAL;
+    if (n_groups == 0) return MOE_W4_OK;
+    if (!offsets || !dw || (M > 0 && (!x || !dy))) return MOE_W4_EINVAL;   // M == 0: dw is add, or zeros
+    const size_t nw = (size_t)(n_groups * N * K) * elem_bytes(dw_dtype);
+    const Span in[] = {{M > 0 ? x : nullptr, (size_t)(M * K) * 2, 16}, {M > 0 ? dy : nullptr, (size_t)(M * N) * 2, 16},
+                       {offsets, (size_t)(n_groups + 1) * 4, 4}, {add == dw ? nullptr : add, nw, 16}};
+    const Span out[] = {{dw, nw, 16}};
+    if (!all_aligned(in) || !all_aligned(out) || !outputs_apart(in, out)) return MOE_W4_EINVAL;
+    (void)hipGetLastError();
+    launch_grouped_mm_dw(x, dy, offsets, (int)n_groups, (int)M, (int)N, (int)K, dtype == MOE_W4_BF16,
+                         dw_dtype == MOE_W4_F32, add, dw, static_cast<hipStream_t>(stream));
+    return device_status(hipGetLastError());
+}
+
+size_t moe_w4_matvec_workspace_bytes(int64_t M, int64_t K) {
+    if (M < 0 || M > MOE_W4_MATVEC_MAX_TOKENS || K < 128 || K > MOE_W4_MATVEC_MAX_K || K % 128 != 0) return 0;
+    return matvec_workspace_bytes((int)M, (int)K);
+}
+
+int moe_w4_matvec(const void *x, const void *codes, const void *scales, int64_t M, int64_t N, int64_t K, int group,
+                  int rotate, int x_dtype, void *y, int y_dtype, void *workspace, size_t workspace_bytes,
+                  void *stream) {
+    if (M < 0 || M > MOE_W4_MATVEC_MAX_TOKENS || N < 0 || N > MOE_W4_MATVEC_MAX_N || K < 128 ||
+        K > MOE_W4_MATVEC_MAX_K || K % 128 != 0 || (group != 32 && group != 64 && group != 128) || !is_elem16(x_dtype) ||
+        !is_elem(y_dtype))
+        return MOE_W4_EINVAL;
+    if (M == 0 || N == 0) return MOE_W4_OK;
+    if (!x || !codes || !scales || !y || !workspace) return MOE_W4_EINVAL;
+    const Span in[] = {{x, (size_t)(M * K) * 2, 16}, {codes, (size_t)(N * K / 2), 16},
+                       {scales, (size_t)(N * (K / group)) * 2, 2}};
+    const Span out[] = {{y, (size_t)(M * N) * elem_bytes(y_dtype), 16}, {workspace, workspace_bytes, 16}};
+    if (!all_aligned(in) || !all_aligned(out)) return MOE_W4_EINVAL;
+    if (workspace_bytes < matvec_workspace_bytes((int)M, (int)K)) return MOE_W4_EWORKSPACE;
+    if (!outputs_apart(in, out)) return MOE_W4_EINVAL;
+    const MatvecArgs a{x, static_cast<const uint8_t *>(codes), static_cast<const uint16_t *>(scales), y, workspace,
+                       (int)M, (int)N, (int)K, group, rotate != 0, x_dtype, y_dtype};
+    (void)hipGetLastError();
+    launch_matvec(a, static_cast<hipStream_t>(stream));
+    return device_status(hipGetLastError());
+}
+
+int moe_w4_norm_residual(const void *resid, const void *y, const void *gate, int gate_kind, float scale,
+                         const void *post_gain, const void *pre_gain, int flags, float eps, int64_t T, int64_t H,
+                         int dtype, int resid_dtype, void *resid_out, void *x_out, void *stream) {
+    if (!norm_form_ok(y, gate, gate_kind, scale, post_gain, pre_gain, flags, eps, T, H, dtype, resid_dtype))
+        return MOE_W4_EINVAL;
+    if (T == 0) return MOE_W4_OK;
+    const bool pre = flags & MOE_W4_NORM_PRE;
+    if (!resid || (y != nullptr) != (resid_out != nullptr) || pre != (x_out != nullptr)) return MOE_W4_EINVAL;
+    const size_t nr = (size_t)(T * H) * elem_bytes(resid_dtype), b = elem_bytes(dtype), na = (size_t)(T * H) * b;
+    const Span in[] = {{resid == resid_out ? nullptr : resid, nr, 16}, {y, na, 16},
+                       {gate, gate_elems(gate_kind, T, H) * b, 16}, {post_gain, (size_t)H * b, 16},
+                       {pre_gain, (size_t)H * b, 16}};
+    const Span out[] = {{resid_out, nr, 16}, {x_out, na, 16}};
+    if (!aligned(resid, MOE_W4_ALIGN) || !all_aligned(in) || !all_aligned(out) || !outputs_apart(in, out))
+        return MOE_W4_EINVAL;
+    const NormArgs a{resid, y, gate, post_gain, pre_gain, resid_out, x_out, T, (int)H, gate_kind, flags, scale, eps};
+    (void)hipGetLastError();
+    launch_norm_residual(a, dtype, resid_dtype, static_cast<hipStream_t>(stream));
+    return device_status(hipGetLastError());
+}
+
+size_t moe_w4_norm_workspace_bytes(int64_t T, int64_t H) {
+    return norm_sizes_ok(T, H) ? align_up((size_t)3 * norm_back_slices(T, (int)H) * (size_t)H * 4) + 256 : 0;
+}
+
+int moe_w4_norm_residual_backward(const void *resid_out, const void *y, const void *gate, int gate_kind, float scale,
+                                  const void *post_gain, const void *pre_gain, int flags, float eps, int64_t T,
+                                  int64_t H, int dtype, int resid_dtype, const void *d_resid_out, const void *d_x,
+                                  void *d_resid, void *d_y, void *d_gate, float *d_post_gain, float *d_pre_gain,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    if (!norm_form_ok(y, gate, gate_kind, scale, post_gain, pre_gain, flags, eps, T, H, dtype, resid_dtype))
+        return MOE_W4_EINVAL;
+    const bool pre = flags & MOE_W4_NORM_PRE, post = flags & MOE_W4_NORM_POST;
+    if ((d_pre_gain && !pre) || (d_post_gain && !post) || (d_gate && gate_kind == MOE_W4_GATE_NONE)) return MOE_W4_EINVAL;
+    if (T > 0 && (!d_resid || (pre && !resid_out) || pre != (d_x != nullptr) || (y != nullptr) != (d_y != nullptr)))
+        return MOE_W4_EINVAL;
+    if (!workspace) return MOE_W4_EINVAL;
+    const size_t nr = (size_t)(T * H) * elem_bytes(resid_dtype), b = elem_bytes(dtype), na = (size_t)(T * H) * b;
+    const size_t ng = gate_elems(gate_kind, T, H), nh = (size_t)H * 4;
+    const Span in[] = {{resid_out, nr, 16}, {y, na, 16}, {gate, ng * b, 16}, {post_gain, (size_t)H * b, 16},
+                       {pre_gain, (size_t)H * b, 16}, {d_resid_out == d_resid ? nullptr : d_resid_out, nr, 16},
+                       {d_x, na, 16}};
+    const Span out[] = {{d_resid, nr, 16}, {d_y, na, 16}, {d_gate, ng * (gate_kind == MOE_W4_GATE_FULL ? b : 4), 16},
+                        {d_post_gain, nh, 16}, {d_pre_gain, nh, 16}, {workspace, workspace_bytes, 16}};
+    if (!all_aligned(in) || !all_aligned(out)) return MOE_W4_EINVAL;
+    if (workspace_bytes < moe_w4_norm_workspace_bytes(T, H)) return MOE_W4_EWORKSPACE;
+    if (!outputs_apart(in, out)) return MOE_W4_EINVAL;
+    const NormBackArgs a{resid_out, y, gate, post_gain, pre_gain, d_resid_out, d_x, d_resid, d_y, d_gate,
+                         d_post_gain, d_pre_gain, static_cast<float *>(workspace), T, (int)H, gate_kind, flags, scale, eps};
+    (void)hipGetLastError();
+    launch_norm_residual_backward(a, dtype, resid_dtype, static_cast<hipStream_t>(stream));
     return device_status(hipGetLastError());
 }
 

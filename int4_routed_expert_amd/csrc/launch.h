@@ -201,6 +201,54 @@ void launch_down_nvfp4(const uint8_t *codes, const uint8_t *scales, const float 
 void launch_rmsnorm_bf16(const float *resid, int T, uint16_t *x, hipStream_t s);
 void launch_residual_add(float *resid, const uint16_t *y, int T, hipStream_t s);
 
+// Element types of the block operators (MOE_W4_F32, _BF16, _F16).
+enum ElemType { kElemF32 = 0, kElemBf16 = 1, kElemF16 = 2 };
+
+// Products grouped by expert (16-bit elements; n and k multiples of 8):
+// y = x w^T, dx = dy w, dw = (add +) dy^T x over the rows of each group.
+void launch_grouped_mm(const void *x, const void *w, const int *offsets, int groups, int rows, int n, int k, bool bf16,
+                       void *y, hipStream_t s);
+void launch_grouped_mm_dx(const void *dy, const void *w, const int *offsets, int groups, int rows, int n, int k, bool bf16,
+                          void *dx, hipStream_t s);
+void launch_grouped_mm_dw(const void *x, const void *dy, const int *offsets, int groups, int rows, int n, int k, bool bf16,
+                          bool f32_out, const void *add, void *dw, hipStream_t s);
+
+// The norms around a block with its gate and residual scale (norm.hip).
+enum GateKind { kGateNone = 0, kGateToken = 1, kGateChannel = 2, kGateFull = 3 };
+enum NormFlags { kNormPost = 1, kNormPre = 2 };
+struct NormArgs {
+    const void *resid, *y, *gate, *post_gain, *pre_gain;
+    void *resid_out, *x_out;
+    int64_t T;
+    int H, gate_kind, flags;
+    float scale, eps;
+};
+struct NormBackArgs {
+    const void *resid_out, *y, *gate, *post_gain, *pre_gain, *d_resid_out, *d_x;
+    void *d_resid, *d_y, *d_gate;
+    float *d_post_gain, *d_pre_gain, *parts;   // parts: [3][norm_back_slices][H]
+    int64_t T;
+    int H, gate_kind, flags;
+    float scale, eps;
+};
+void launch_norm_residual(const NormArgs &a, int act, int res, hipStream_t s);
+int norm_back_slices(int64_t T, int H);
+void launch_norm_residual_backward(const NormBackArgs &a, int act, int res, hipStream_t s);
+
+// Products of int4 weight rows with up to kMatvecMaxTokens tokens (matvec.hip).
+constexpr int kMatvecMaxTokens = 64;
+struct MatvecArgs {
+    const void *x;
+    const uint8_t *codes;     // [n][k / 2]
+    const uint16_t *scales;   // bf16 [n][k / group]
+    void *y, *ws;
+    int m, n, k, group;
+    bool rotate;
+    int x_type, y_type;
+};
+size_t matvec_workspace_bytes(int m, int k);
+void launch_matvec(const MatvecArgs &a, hipStream_t s);
+
 // Seeded generator.
 void launch_gen_normal_bf16(uint64_t key, int64_t n, float mult, int absval, uint16_t *out, hipStream_t s);
 void launch_gen_codes(uint64_t key, int rows, int k, int experts, int64_t expert_elems,
