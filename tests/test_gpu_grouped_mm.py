@@ -79,6 +79,47 @@ def test_three_products(m, counts, n, k, dtype):
         assert bool((t[:3] == 7).all()) and bool((t[int(off[-1]):] == 7).all())
 
 
+# sizes whose tiles are the largest ones of each product (many rows a group and many tiles), the ones between, and
+# the smallest, each with ragged edges in every direction
+@pytest.mark.parametrize("which,groups,each,n,k", [("mm", 20, 300, 2056, 264), ("mm", 4, 700, 1032, 136), ("mm", 6, 200, 264, 72),
+                                                   ("mm", 40, 60, 648, 200), ("mm", 70, 3, 520, 264),
+                                                   ("dx", 20, 300, 264, 2056), ("dx", 4, 700, 136, 1032), ("dx", 40, 60, 200, 648),
+                                                   ("dw", 60, 90, 1400, 2056), ("dw", 5, 400, 1288, 520)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_tile_forms(m, which, groups, each, n, k, dtype):
+    rng = np.random.default_rng(groups + n)
+    counts = rng.multinomial(groups * each, np.ones(groups) / groups)
+    counts[groups // 2] = 0
+    counts[-1] = 1
+    off, x, dy, w = make(counts.tolist(), n, k, dtype, 13, behind=40)
+    offsets, x, dy, w = torch.from_numpy(off).cuda(), x.cuda(), dy.cuda(), w.cuda()
+    src, out = (x, torch.full((x.shape[0], n), 7.0, dtype=DT[dtype], device="cuda")) if which == "mm" else \
+        (dy, torch.full((x.shape[0], k), 7.0, dtype=DT[dtype], device="cuda"))
+    if which == "dw":
+        add = torch.randn(w.shape, device="cuda")
+        out = torch.full(w.shape, 7.0, device="cuda")
+        m.moe_w4_grouped_mm_dw(x, dy, offsets, out, add=add)
+        half = torch.full_like(w, 7.0)
+        m.moe_w4_grouped_mm_dw(x, dy, offsets, half)
+    elif which == "mm":
+        m.moe_w4_grouped_mm(x, w, offsets, out)
+    else:
+        m.moe_w4_grouped_mm_dx(dy, w, offsets, out)
+    for e in range(groups):
+        a, b = int(off[e]), int(off[e + 1])
+        W = w[e].double()
+        if which == "dw":
+            ref, mag = dy[a:b].double().t() @ x[a:b].double(), dy[a:b].double().abs().t() @ x[a:b].double().abs()
+            check(out[e], (ref + add[e].double()).cpu(), (mag + add[e].double().abs()).cpu(), b - a + 1, "f32", f"dw group {e}")
+            check(half[e], ref.cpu(), mag.cpu(), b - a, dtype, f"16-bit dw group {e}")
+            continue
+        W = W.t() if which == "mm" else W
+        S = src[a:b].double()
+        check(out[a:b], (S @ W).cpu(), (S.abs() @ W.abs()).cpu(), W.shape[0], dtype, f"{which} group {e}")
+    if which != "dw":
+        assert bool((out[int(off[-1]):] == 7).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_dw_adds_in_its_own_type(m, dtype):
     off, x, dy, w = make([5, 0, 130], 40, 72, dtype, 3)
