@@ -409,8 +409,9 @@ int moe_w4_grouped_mm_dw(const void *x, const void *dy, const int32_t *offsets, 
  * K: a multiple of 128 up to MOE_W4_MATVEC_MAX_K; N: 0 ..
  * MOE_W4_MATVEC_MAX_N (0, or M == 0: nothing is enqueued).  workspace: at least
  * moe_w4_matvec_workspace_bytes(M, K) bytes, contents on entry irrelevant.
- * Pointers 16-byte aligned (scales 2); y overlaps no input and not the
- * workspace.  EINVAL / EWORKSPACE otherwise. */
+ * Pointers 16-byte aligned (scales 256 / group); y overlaps no input and not
+ * the workspace.  A token whose x is not finite has results that are not
+ * finite.  EINVAL / EWORKSPACE otherwise. */
 #define MOE_W4_MATVEC_MAX_TOKENS 64
 #define MOE_W4_MATVEC_MAX_K 65536
 #define MOE_W4_MATVEC_MAX_N 16777216

@@ -891,7 +891,7 @@ int moe_w4_matvec(const void *x, const void *codes, const void *scales, int64_t 
     if (M == 0 || N == 0) return MOE_W4_OK;
     if (!x || !codes || !scales || !y || !workspace) return MOE_W4_EINVAL;
     const Span in[] = {{x, (size_t)(M * K) * 2, 16}, {codes, (size_t)(N * K / 2), 16},
-                       {scales, (size_t)(N * (K / group)) * 2, 2}};
+                       {scales, (size_t)(N * (K / group)) * 2, (size_t)(256 / group)}};   // (a block's scales are one load)
     const Span out[] = {{y, (size_t)(M * N) * elem_bytes(y_dtype), 16}, {workspace, workspace_bytes, 16}};
     if (!all_aligned(in) || !all_aligned(out)) return MOE_W4_EINVAL;
     if (workspace_bytes < matvec_workspace_bytes((int)M, (int)K)) return MOE_W4_EWORKSPACE;

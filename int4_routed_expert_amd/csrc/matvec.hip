@@ -8,19 +8,37 @@
 //
 // Exactness: code c enters as the bf16 value 24 + c (16 <= . < 32: the nibble,
 // its sign bit flipped, in mantissa bits 3..6 of 16.0), and 24 sum(x) is taken
-// off by starting each group's sums at x times a constant -24 operand.  x enters
-// as 1 to 3 bf16 columns that add up to it (bf16 is itself; fp16 and rotated
-// values are two, 16 bits, or three, 24 bits, for fp32 results), so every
+// off by starting each group's sums at -24 times the sum of x over the group.  x
+// enters as 1 to 3 bf16 columns that add up to it (bf16 is itself; fp16 and
+// rotated values are two, 16 bits, or three, 24 bits, for fp32 results), so every
 // product is exact and only the fp32 sums round.
+//
+// Work: a workgroup takes a run of 16-row tiles and makes one sequence of their
+// 128-blocks of K, of which its waves take equal parts, so that neither few rows
+// nor an odd number of tiles leaves waves idle; where a tile's blocks fall to
+// several waves, their sums meet in LDS at the end, in order.
+//
+// One launch, if the operands of x fit LDS: each workgroup makes them there while
+// its first weights are on their way.  Otherwise a launch before makes them in the
+// workspace, and the waves read them through the caches.
+#include <type_traits>
+
 #include "common.h"
 #include "launch.h"
 
 namespace moe_w4 {
 
+struct MatvecPlan {
+    int cols;       // columns of x
+    int tiles;      // 16-row tiles
+};
+
 namespace {
 
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+constexpr int kLdsBytes = 160 * 1024;
 
 __device__ __forceinline__ f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
@@ -33,7 +51,6 @@ __device__ __forceinline__ uint4 codes_to_bf16(uint32_t w) {
     return make_uint4(((w << 3) & kField) ^ kSixteen, ((w >> 1) & kField) ^ kSixteen, ((w >> 5) & kField) ^ kSixteen,
                       ((w >> 9) & kField) ^ kSixteen);
 }
-constexpr uint32_t kMinus24 = 0xc1c0c1c0u;   // two bf16 -24
 
 // Lane 16 g + t holds four dwords; afterwards dword i of lane 16 g + t is dword g of lane 16 i + t.
 __device__ __forceinline__ void transpose4(uint4 &v) {
@@ -46,106 +63,253 @@ __device__ __forceinline__ void transpose4(uint4 &v) {
 
 __device__ __forceinline__ uint32_t bf16_bits(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
 
-// Columns of x: tile c / 16 of kTile = 16 / parts tokens.
-constexpr int tokens_per_tile(int parts) { return 16 / parts; }
+// A token takes as many columns as its parts (three: four, the last unused), so
+// that its parts' sums meet in one lane.
+constexpr int column_stride(int parts) { return parts == 3 ? 4 : parts; }
 
-}  // namespace
-
-// x -> MFMA operands in ws: [column tile][k / 32][lane][8 bf16], lane 16 g + c
-// holding k = 32 i + 8 g .. + 8 of column c in the order of codes_to_bf16.  16
-// lanes a 128-block of a token.
-template <bool BF16, int PARTS>
-__global__ __launch_bounds__(256) void k_matvec_x(const uint16_t *__restrict__ x, int m, int k, bool rotate, uint4 *ws) {
-    const int blocks = k / 128;
-    const int item = blockIdx.x * 16 + (threadIdx.x >> 4), j = threadIdx.x & 15;
-    const bool live = item < m * blocks;
-    const int tok = live ? item / blocks : 0, blk = live ? item % blocks : 0;
-    const uint4 q = *reinterpret_cast<const uint4 *>(x + (size_t)tok * k + blk * 128 + j * 8);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-    float v[8];
+// Operands of blocks [b0, b0 + n) of x: xs[block][4][4][cols] of 16 bytes (element (i,
+// g, c): k = 32 i + 8 g .. + 8 of the block, column c, in the order of
+// codes_to_bf16) and starts[group][16 CT], -24 times each group's sum.  Called by
+// whole waves, `step` threads in all, this one number tid of them.
+template <int GROUP, int CT, int PARTS>
+__device__ __forceinline__ void make_operands(const MatvecArgs &a, int cols, int b0, int n, int tid, int step, uint4 *xs,
+                                              float *starts) {
+    constexpr int kGroups = 128 / GROUP, kStride = column_stride(PARTS), kTokens = 16 / kStride;
+    const int places = n * 16;   // 8 elements each, 16 to a block; a thread keeps its place and walks the tokens
+    const int at_once = max(step / places, 1);
+    constexpr int kAhead = 4;    // tokens loaded together
+    for (int place = step >= places ? tid % places : tid; place < places; place += step >= places ? places : step) {
+        const int j = place & 15, blk = place >> 4, tok0 = step >= places ? tid / places : 0;
+        if (tok0 >= at_once) break;
+        const uint16_t *from = static_cast<const uint16_t *>(a.x) + (size_t)(b0 + blk) * 128 + j * 8;
+        for (int tok = tok0; tok < a.m; tok += kAhead * at_once) {
+            uint4 q[kAhead];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = BF16 ? bf16lo(w[i]) : half_lo(w[i]);
-        v[2 * i + 1] = BF16 ? bf16hi(w[i]) : half_hi(w[i]);
-    }
-    if (rotate) fwht128_lanes16(v, threadIdx.x & 63);
-    if (!live) return;
-    constexpr int kTokens = tokens_per_tile(PARTS);
-    const int tile = tok / kTokens, c = (tok % kTokens) * PARTS;
-    uint4 *out = ws + ((size_t)tile * (k / 32) + blk * 4 + j / 4) * 64 + (j & 3) * 16 + c;
+            for (int u = 0; u < kAhead; ++u)
+                q[u] = *reinterpret_cast<const uint4 *>(from + (size_t)min(tok + u * at_once, a.m - 1) * a.k);
 #pragma unroll
-    for (int p = 0; p < PARTS; ++p) {
-        uint32_t b[8];
+            for (int u = 0; u < kAhead; ++u) {
+                const int token = tok + u * at_once;
+                if (token >= a.m) break;
+                const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
+                float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            b[i] = bf16_bits(v[i]);
-            v[i] -= __uint_as_float(b[i] << 16);
-        }
-        out[p] = make_uint4(b[0] | (b[4] << 16), b[1] | (b[5] << 16), b[2] | (b[6] << 16), b[3] | (b[7] << 16));
-    }
-}
-
-// 16 weight rows and CT column tiles a workgroup, its WAVES waves taking every
-// WAVES-th 128-block of K; their sums are added in order through LDS.
-template <int GROUP, int CT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void k_matvec(MatvecArgs a, int parts, int tiles) {
-    __shared__ f32x4_t red[WAVES][CT][64];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int t = lane & 15, g = lane >> 4;
-    const int n0 = blockIdx.x * 16, ct0 = blockIdx.y * CT;
-    const int blocks = a.k / 128, chunks = a.k / 32;
-    constexpr int kGroups = 128 / GROUP, kPer = GROUP / 32;
-    const int row = min(n0 + t, a.n - 1);   // rows behind the last are computed and not stored
-    const uint4 *codes = reinterpret_cast<const uint4 *>(a.codes + (size_t)row * (a.k / 2)) + g;
-    const uint16_t *scales = a.scales + (size_t)row * (a.k / GROUP);
-    const uint4 *xf[CT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c)
-        xf[c] = static_cast<const uint4 *>(a.ws) + (size_t)min(ct0 + c, tiles - 1) * chunks * 64 + lane;
-    f32x4_t sum[CT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) sum[c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int b = wave; b < blocks; b += WAVES) {
-        uint4 w = codes[b * 4];
-        transpose4(w);
-        const uint32_t wd[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int gr = 0; gr < kGroups; ++gr) {
-            const float s = bf16_to_f32(scales[b * kGroups + gr]);
-            uint4 q[kPer];
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) q[i] = codes_to_bf16(wd[gr * kPer + i]);
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                f32x4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
-                uint4 xv[kPer];
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {
-                    xv[i] = xf[c][(size_t)(b * 4 + gr * kPer + i) * 64];
-                    acc = mfma16(xv[i], make_uint4(kMinus24, kMinus24, kMinus24, kMinus24), acc);
+                for (int i = 0; i < 4; ++i) {
+                    v[2 * i] = a.x_type == kElemBf16 ? bf16lo(w[i]) : half_lo(w[i]);
+                    v[2 * i + 1] = a.x_type == kElemBf16 ? bf16hi(w[i]) : half_hi(w[i]);
                 }
+                if (a.rotate) fwht128_lanes16(v, tid & 63);   // (the 16 lanes of a block take every branch here together)
+                const int col = (token / kTokens) * 16 + (token % kTokens) * kStride;
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) acc = mfma16(xv[i], q[i], acc);
-                sum[c] += s * acc;
+                for (int p = 0; p < PARTS; ++p) {
+                    uint32_t b[8];
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        b[i] = bf16_bits(v[i]);
+                        const float h = __uint_as_float(b[i] << 16);
+                        sum += h;
+                        v[i] -= h;
+                    }
+#pragma unroll
+                    for (int d = 1; d < GROUP / 8; d <<= 1) sum += shfl_xor_f(sum, d);
+                    xs[place * cols + col + p] =
+                        make_uint4(b[0] | (b[4] << 16), b[1] | (b[5] << 16), b[2] | (b[6] << 16), b[3] | (b[7] << 16));
+                    if (j % (GROUP / 8) == 0) starts[(blk * kGroups + j / (GROUP / 8)) * (16 * CT) + col + p] = -24.0f * sum;
+                }
             }
         }
     }
+}
+
+}  // namespace
+
+// All operands of x into the workspace: xs of every block, then starts.
+template <int GROUP, int CT, int PARTS>
+__global__ __launch_bounds__(256) void k_matvec_x(MatvecArgs a, MatvecPlan plan) {
+    const int blocks = a.k / 128;
+    uint4 *xs = static_cast<uint4 *>(a.ws);
+    make_operands<GROUP, CT, PARTS>(a, plan.cols, 0, blocks, blockIdx.x * 256 + threadIdx.x, gridDim.x * 256, xs,
+                                    reinterpret_cast<float *>(xs + (size_t)blocks * 16 * plan.cols));
+}
+
+// Waves of a workgroup, and waves a SIMD that the registers are cut for.  One
+// column tile: two workgroups of 8 a CU.  Two: one of 16, as x fills LDS.  More need
+// the registers of two waves a SIMD.  Where a wave keeps the sums of its head (the
+// last blocks of a tile that others begin) until the end: in registers, and with more
+// column tiles in LDS, behind x.
+constexpr int waves_of(int ct) { return ct == 2 ? 16 : 8; }
+constexpr int simd_waves(int ct) { return ct <= 2 ? 4 : 2; }
+constexpr bool head_in_lds(int ct) { return ct > 2; }
+
+// PARTS parts of x; CT tiles of 16 columns; LDS: x's operands (xs, then starts) are
+// there.  The waves' sums take their place, or follow.
+template <int GROUP, int CT, int PARTS, bool LDS>
+__global__ __launch_bounds__(64 * waves_of(CT), simd_waves(CT)) void k_matvec(MatvecArgs a, MatvecPlan plan) {
+    extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+    constexpr int kWaves = waves_of(CT);
+    constexpr int kGroups = 128 / GROUP, kPer = GROUP / 32;   // groups a block, MFMAs a group
+    constexpr int kStride = column_stride(PARTS), kTokens = 16 / kStride;
+    constexpr int kBatch = 2;   // blocks whose weights a wave loads at a time, two such batches in flight
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int t = lane & 15, g = lane >> 4;
+    const int blocks = a.k / 128;
+    const int cols = CT == 1 ? plan.cols : 16 * CT;
+    uint4 *xs = reinterpret_cast<uint4 *>(smem);
+    float *starts = reinterpret_cast<float *>(smem + (size_t)blocks * 256 * cols);
+    const uint4 *xw = static_cast<const uint4 *>(a.ws);
+    const float *startsw = reinterpret_cast<const float *>(xw + (size_t)blocks * 16 * cols);
+
+    // tiles [tile0, tile1) of this workgroup; of their blocks in a row this wave's [begin, end)
+    const int tile0 = (int)((int64_t)plan.tiles * blockIdx.x / gridDim.x), tile1 = (int)((int64_t)plan.tiles * (blockIdx.x + 1) / gridDim.x);
+    const int all = (tile1 - tile0) * blocks;
+    auto part = [&](int w) { return (int)((int64_t)all * w / kWaves); };
+    const int begin = __builtin_amdgcn_readfirstlane(part(wave)), end = __builtin_amdgcn_readfirstlane(part(wave + 1));
+
+    // A batch: n blocks from block b of a tile.
+    struct Place {
+        int tile, b, n, left;   // left: this wave's blocks from here on
+    };
+    auto fill = [&](Place &p) { p.n = min(min(kBatch, blocks - p.b), p.left); };
+    auto next = [&](Place &p) {
+        p.left -= p.n;
+        p.b += p.n;
+        if (p.b == blocks) p.b = 0, ++p.tile;
+        fill(p);
+    };
+    struct Batch {
+        uint4 codes[kBatch];
+        uint32_t scales[kBatch][GROUP == 32 ? 2 : 1];
+    };
+    // a lane's byte in its 16 rows; rows behind the last are out of the buffers' range and read as zeros
+    const uint32_t code_pitch = (uint32_t)a.k / 2, scale_pitch = (uint32_t)a.k / GROUP * 2;
+    const uint32_t code_at = t * code_pitch + 16 * g, scale_at = t * scale_pitch;
+    auto load = [&](Batch &w, const Place &p) {
+        const int64_t row = (int64_t)p.tile * 16;
+        const uint32_t left = (uint32_t)max(0, min(16, a.n - (int)row));
+        const __amdgpu_buffer_rsrc_t codes = make_buf(a.codes + row * code_pitch, left * code_pitch);
+        const __amdgpu_buffer_rsrc_t scales = make_buf(reinterpret_cast<const uint8_t *>(a.scales) + row * scale_pitch, left * scale_pitch);
 #pragma unroll
-    for (int c = 0; c < CT; ++c) red[wave][c][lane] = sum[c];
+        for (int u = 0; u < kBatch; ++u) {
+            if (u >= p.n) break;
+            const uint32_t b = p.b + u;
+            w.codes[u] = bload16_nt(codes, code_at + b * 64, 0);
+            if constexpr (GROUP == 32) {
+                w.scales[u][0] = bload4(scales, scale_at + b * 8, 0);
+                w.scales[u][1] = bload4(scales, scale_at + b * 8 + 4, 0);
+            } else if constexpr (GROUP == 64) {
+                w.scales[u][0] = bload4(scales, scale_at + b * 4, 0);
+            } else {
+                w.scales[u][0] = bload2(scales, scale_at + b * 2, 0);
+            }
+        }
+    };
+
+    constexpr bool kHeadLds = head_in_lds(CT);
+    f32x4_t *red = reinterpret_cast<f32x4_t *>(kHeadLds && LDS ? smem + (size_t)blocks * (256 * cols + kGroups * 64 * CT) : smem);
+    f32x4_t sum[CT], head[kHeadLds ? 1 : CT];   // of the tile at hand; of the head
+#pragma unroll
+    for (int c = 0; c < CT; ++c) sum[c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const bool has_head = begin < end && begin % blocks != 0;
+    auto block = [&](Batch &w, int u, int b) {
+        transpose4(w.codes[u]);
+        const uint32_t wd[4] = {w.codes[u].x, w.codes[u].y, w.codes[u].z, w.codes[u].w};
+        const int at = (b * 16 + g) * cols + (CT == 1 ? min(t, cols - 1) : t);
+        const int st = b * kGroups * (16 * CT) + 4 * g;
+#pragma unroll
+        for (int gr = 0; gr < kGroups; ++gr) {
+            const float s = (gr & 1) ? bf16hi(w.scales[u][gr >> 1]) : bf16lo(w.scales[u][gr >> 1]);
+            uint4 q[kPer];
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) q[k] = codes_to_bf16(wd[gr * kPer + k]);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                f32x4_t acc = *reinterpret_cast<const f32x4_t *>((LDS ? starts : startsw) + st + (gr * CT + c) * 16);
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) acc = mfma16((LDS ? xs : xw)[at + (gr * kPer + k) * 4 * cols + c * 16], q[k], acc);
+                sum[c] += s * acc;
+            }
+        }
+    };
+    auto store = [&](int tile) {   // element i of sum[c] is column 16 c + 4 g + i of row t
+        const int row = tile * 16 + t;
+        if (row >= a.n) return;
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; i += kStride) {
+                const int token = c * kTokens + (4 * g + i) / kStride;
+                if (token >= a.m) continue;
+                float v = sum[c][i];
+                if (PARTS > 1) v += sum[c][i + 1];
+                if (PARTS > 2) v += sum[c][i + 2];
+                const size_t o = (size_t)token * a.n + row;
+                if (a.y_type == kElemF32) static_cast<float *>(a.y)[o] = v;
+                else if (a.y_type == kElemF16) static_cast<_Float16 *>(a.y)[o] = (_Float16)v;
+                else static_cast<uint16_t *>(a.y)[o] = (uint16_t)bf16_bits(v);
+            }
+    };
+    auto compute = [&](Batch &w, const Place &p) {
+        if (p.n == kBatch) {   // no branch between the blocks: their loads and products overlap
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) block(w, u, p.b + u);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+                if (u < p.n) block(w, u, p.b + u);
+        }
+        if (p.b + p.n < blocks) return;
+        // the tile's last block: it is whole, or (the first one) the head
+        const bool is_head = has_head && p.tile == tile0 + begin / blocks;
+        if (!is_head) store(p.tile);
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+            if (is_head) {
+                if constexpr (kHeadLds) red[(wave * CT + c) * 64 + lane] = sum[c];
+                else head[c] = sum[c];
+            }
+            sum[c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+    };
+
+    // products one batch behind the loads
+    Place p{tile0 + begin / blocks, begin % blocks, 0, end - begin};
+    fill(p);
+    Batch w0, w1;
+    load(w0, p);
+    if constexpr (LDS) {
+        make_operands<GROUP, CT, PARTS>(a, cols, 0, blocks, tid, 64 * kWaves, xs, starts);
+        __syncthreads();
+    }
+    while (p.left > 0) {
+        Place p1 = p;
+        next(p1);
+        load(w1, p1);
+        compute(w0, p);
+        if (p1.left <= 0) break;
+        p = p1;
+        next(p);
+        load(w0, p);
+        compute(w1, p1);
+    }
+
+    // Tiles that several waves share: the wave with the first blocks adds the others' sums.
+    const bool middle = has_head && begin / blocks == (end - 1) / blocks && end % blocks != 0;   // neither end is this wave's
+    const bool has_tail = begin < end && end % blocks != 0 && !middle;
+    if (!kHeadLds) __syncthreads();   // the sums take the place of x
+    if (has_head && (middle || !kHeadLds)) {
+#pragma unroll
+        for (int c = 0; c < CT; ++c) red[(wave * CT + c) * 64 + lane] = middle || kHeadLds ? sum[c] : head[kHeadLds ? 0 : c];
+    }
     __syncthreads();
-    // column 4 g + i of row t is element i of lane 16 g + t
-    const int per_tile = 16 / parts;
-    for (int o = threadIdx.x; o < CT * per_tile * 16; o += 64 * WAVES) {
-        const int r = o & 15, tok = o >> 4, c = tok / per_tile, col = (tok % per_tile) * parts;
-        const int token = (ct0 + c) * per_tile + tok % per_tile;
-        if (n0 + r >= a.n || token >= a.m) continue;
-        float v = 0.0f;
-        for (int p = 0; p < parts; ++p)
-            for (int wv = 0; wv < WAVES; ++wv) v += red[wv][c][((col + p) >> 2) * 16 + r][(col + p) & 3];
-        const size_t at = (size_t)token * a.n + n0 + r;
-        if (a.y_type == kElemF32) static_cast<float *>(a.y)[at] = v;
-        else if (a.y_type == kElemF16) static_cast<_Float16 *>(a.y)[at] = (_Float16)v;
-        else static_cast<uint16_t *>(a.y)[at] = (uint16_t)bf16_bits(v);
+    if (has_tail) {
+        const int tile = (end - 1) / blocks, stop = (tile + 1) * blocks;
+        for (int w = wave + 1; w < kWaves && part(w) < stop; ++w) {
+            if (part(w) == part(w + 1)) continue;   // no blocks
+#pragma unroll
+            for (int c = 0; c < CT; ++c) sum[c] += red[(w * CT + c) * 64 + lane];
+        }
+        store(tile0 + tile);
     }
 }
 
@@ -155,37 +319,77 @@ static int x_parts(const MatvecArgs &a) {
     return a.x_type == kElemBf16 ? 1 : 2;
 }
 
-size_t matvec_workspace_bytes(int m, int k) {
-    const int per = tokens_per_tile(3);
-    return (size_t)((m + per - 1) / per) * (size_t)k * 32 + 256;
+// Column tiles of m tokens of `parts` parts: 1, 2, 4, 8 or 16.
+static int column_tiles(int m, int parts) {
+    const int tokens = 16 / column_stride(parts), want = (m + tokens - 1) / tokens;
+    return want <= 1 ? 1 : want <= 2 ? 2 : want <= 4 ? 4 : want <= 8 ? 8 : 16;
 }
 
-template <int GROUP>
-static void launch_group(const MatvecArgs &a, int parts, int tiles, hipStream_t s) {
-    const unsigned gx = (unsigned)((a.n + 15) / 16);
-    if (tiles == 1)
-        hipLaunchKernelGGL((k_matvec<GROUP, 1, 4>), dim3(gx, 1), dim3(256), 0, s, a, parts, tiles);
-    else if (tiles == 2)
-        hipLaunchKernelGGL((k_matvec<GROUP, 2, 4>), dim3(gx, 1), dim3(256), 0, s, a, parts, tiles);
-    else
-        hipLaunchKernelGGL((k_matvec<GROUP, 4, 4>), dim3(gx, (tiles + 3) / 4), dim3(256), 0, s, a, parts, tiles);
+// Room for all operands of m tokens of three parts (a block: 16 columns of 256 bytes,
+// and the starts of its four groups, a column tile).
+size_t matvec_workspace_bytes(int m, int k) { return (size_t)(k / 128) * column_tiles(m, 3) * (16 * 256 + 4 * 64) + 256; }
+
+// Bytes of the operands of m tokens, and whether they fit LDS (with the waves' heads).
+static int64_t x_bytes(const MatvecArgs &a, int m, int parts) {
+    const int ct = column_tiles(m, parts), cols = ct == 1 ? m * column_stride(parts) : 16 * ct;
+    return (int64_t)(a.k / 128) * (256 * cols + (128 / a.group) * 64 * ct);
+}
+static bool x_fits(const MatvecArgs &a, int m, int parts) {
+    const int ct = column_tiles(m, parts);
+    return x_bytes(a, m, parts) + (head_in_lds(ct) ? waves_of(ct) * ct * 1024 : 0) <= kLdsBytes;
 }
 
 void launch_matvec(const MatvecArgs &a, hipStream_t s) {
-    const int parts = x_parts(a), per = tokens_per_tile(parts), tiles = (a.m + per - 1) / per;
-    const dim3 grid((unsigned)((a.m * (a.k / 128) + 15) / 16));
-    const uint16_t *x = static_cast<const uint16_t *>(a.x);
-    uint4 *ws = static_cast<uint4 *>(a.ws);
-    const bool b = a.x_type == kElemBf16;
-    if (parts == 1) hipLaunchKernelGGL((k_matvec_x<true, 1>), grid, dim3(256), 0, s, x, a.m, a.k, a.rotate, ws);
-    else if (parts == 2 && b) hipLaunchKernelGGL((k_matvec_x<true, 2>), grid, dim3(256), 0, s, x, a.m, a.k, a.rotate, ws);
-    else if (parts == 2) hipLaunchKernelGGL((k_matvec_x<false, 2>), grid, dim3(256), 0, s, x, a.m, a.k, a.rotate, ws);
-    else if (b) hipLaunchKernelGGL((k_matvec_x<true, 3>), grid, dim3(256), 0, s, x, a.m, a.k, a.rotate, ws);
-    else hipLaunchKernelGGL((k_matvec_x<false, 3>), grid, dim3(256), 0, s, x, a.m, a.k, a.rotate, ws);
-    if (hipPeekAtLastError() != hipSuccess) return;
-    if (a.group == 32) launch_group<32>(a, parts, tiles, s);
-    else if (a.group == 64) launch_group<64>(a, parts, tiles, s);
-    else launch_group<128>(a, parts, tiles, s);
+    const int parts = x_parts(a), ct = column_tiles(a.m, parts);
+    const bool in_lds = x_fits(a, a.m, parts);
+    // Operands that do not fit LDS, but do in two halves, and many rows to read them
+    // for: the weights are read twice (64 tokens, 150144 x 2048: 107 us against 186 with
+    // x read through the caches; 16 tokens, 2048 x 6144: 27 us against 12)
+    const int half = (a.m + 1) / 2;
+    if (!in_lds && a.n >= 32768 && x_fits(a, half, parts)) {
+        MatvecArgs h = a;
+        h.m = half;
+        launch_matvec(h, s);
+        if (hipPeekAtLastError() != hipSuccess) return;
+        h.m = a.m - half;
+        h.x = static_cast<const uint16_t *>(a.x) + (size_t)half * a.k;
+        h.y = static_cast<uint8_t *>(a.y) + (size_t)half * a.n * (a.y_type == kElemF32 ? 4 : 2);
+        launch_matvec(h, s);
+        return;
+    }
+    MatvecPlan p;
+    p.cols = ct == 1 ? a.m * column_stride(parts) : 16 * ct;
+    p.tiles = (a.n + 15) / 16;
+    const int blocks = a.k / 128, waves = waves_of(ct), join = waves * ct * 1024, x = in_lds ? (int)x_bytes(a, a.m, parts) : 0;
+    const int lds = head_in_lds(ct) ? x + join : x > join ? x : join;
+    // two workgroups of one column tile a CU, if no tile more falls to a CU so
+    const int one = (p.tiles + 255) / 256, two = 2 * ((p.tiles + 511) / 512);
+    const int slots = ct == 1 && kLdsBytes / lds >= 2 && (two <= one || one > 8) ? 512 : 256;
+    const unsigned grid = (unsigned)(p.tiles < slots ? p.tiles : slots);
+    auto go = [&](auto G, auto C, auto P) {
+        if (!in_lds) {
+            hipLaunchKernelGGL((k_matvec_x<G(), C(), P()>), dim3((unsigned)((a.m * blocks + 15) / 16)), dim3(256), 0, s, a, p);
+            if (hipPeekAtLastError() != hipSuccess) return;
+            hipLaunchKernelGGL((k_matvec<G(), C(), P(), false>), dim3(grid), dim3(64 * waves), lds, s, a, p);
+        } else {
+            hipLaunchKernelGGL((k_matvec<G(), C(), P(), true>), dim3(grid), dim3(64 * waves), lds, s, a, p);
+        }
+    };
+    auto by_parts = [&](auto G, auto C) {
+        if (parts == 1) go(G, C, std::integral_constant<int, 1>{});
+        else if (parts == 2) go(G, C, std::integral_constant<int, 2>{});
+        else go(G, C, std::integral_constant<int, 3>{});
+    };
+    auto by_tiles = [&](auto G) {
+        if (ct == 1) by_parts(G, std::integral_constant<int, 1>{});
+        else if (ct == 2) by_parts(G, std::integral_constant<int, 2>{});
+        else if (ct == 4) by_parts(G, std::integral_constant<int, 4>{});
+        else if (ct == 8) by_parts(G, std::integral_constant<int, 8>{});
+        else go(G, std::integral_constant<int, 16>{}, std::integral_constant<int, 3>{});   // (only three parts need so many)
+    };
+    if (a.group == 32) by_tiles(std::integral_constant<int, 32>{});
+    else if (a.group == 64) by_tiles(std::integral_constant<int, 64>{});
+    else by_tiles(std::integral_constant<int, 128>{});
 }
 
 }  // namespace moe_w4

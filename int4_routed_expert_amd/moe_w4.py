@@ -316,88 +316,88 @@ def _refuse(name, why):
     raise MoeW4Error(EINVAL, f"{name}: {why}")
 
 
-def _arg(name, what, t, device, shape, dtypes):
-    """The address of a contiguous tensor of this device, shape and one of these types."""
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        _refuse(name, f"{what} is not a tensor on {device}")
-    if t.dtype not in dtypes:
-        _refuse(name, f"{what} has type {t.dtype}")
-    if t.shape != shape:
-        _refuse(name, f"{what} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if not t.is_contiguous():
-        _refuse(name, f"{what} is not contiguous")
-    return t.data_ptr()
+def _arg(name, what, t, index, shape, dtype):
+    """The address of a contiguous tensor of GPU `index`, of this shape and type."""
+    try:
+        if t.get_device() == index and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        _refuse(name, f"{what} is no tensor")
+    _refuse(name, f"{what} is {t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ', not contiguous'}; "
+                  f"wanted {dtype} {tuple(shape)} on GPU {index}, contiguous")
 
 
-def _gpu(name, what, t, dims):
-    """The device and shape of the tensor that the others of a call go by."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != dims:
-        _refuse(name, f"{what} is not a tensor of {dims} dimensions on a GPU")
-    return t.device, t.shape
+def _main(name, what, t, dims, dtypes):
+    """The GPU, shape and type of the tensor that the others of a call go by."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dims or t.dtype not in dtypes or not t.is_cuda:
+        _refuse(name, f"{what} is no tensor of {dims} dimensions on a GPU of one of the types {dtypes}")
+    return t.get_device(), t.shape, t.dtype
 
 
-def _enqueue(name, device, stream, *args):
-    index = device.index
+def _other(name, what, t, dims, dtypes):
+    """The shape and type of a further tensor that brings sizes or a type of its own."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dims or t.dtype not in dtypes:
+        _refuse(name, f"{what} is no tensor of {dims} dimensions of one of the types {dtypes}")
+    return t.shape, t.dtype
+
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_gpu = torch._C._cuda_getDevice
+
+
+def _enqueue(name, fn, index, stream, args):
+    """fn(*args, stream) with the tensors' GPU current, on its current stream if none is given."""
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(index)
+        stream = _raw_stream(index)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if torch._C._cuda_getDevice() == index:
-        st = getattr(_lib, name)(*args, stream)
+    if _current_gpu() == index:
+        st = fn(*args, stream)
     else:
         with torch.cuda.device(index):
-            st = getattr(_lib, name)(*args, stream)
+            st = fn(*args, stream)
     if st != OK:
         raise MoeW4Error(st, name)
 
 
 _16BIT = (torch.bfloat16, torch.float16)
-_I32 = (torch.int32,)
-_F32 = (torch.float32,)
-_U8 = (torch.uint8,)
+_ANY = (torch.float32, torch.bfloat16, torch.float16)
 _SCALES = (torch.bfloat16, torch.int16)   # int16: the bits, as empty_layer() holds them
-
-
-def _grouped(name, what, rows, w, offsets, out_what, out, transposed, stream):
-    device, (m, cols) = _gpu(name, what, rows, 2)
-    if not isinstance(w, torch.Tensor) or w.dim() != 3:
-        _refuse(name, "w is not a tensor of 3 dimensions")
-    e, n, k = w.shape
-    dt = (rows.dtype,)
-    if rows.dtype not in _16BIT:
-        _refuse(name, f"{what} has type {rows.dtype}")
-    wide, narrow = (n, k) if transposed else (k, n)
-    _enqueue(name, device, stream, _arg(name, what, rows, device, (m, wide), dt),
-             _arg(name, "w", w, device, (e, n, k), dt), _arg(name, "offsets", offsets, device, (e + 1,), _I32), e, m, n, k,
-             _ELEM[rows.dtype], _arg(name, out_what, out, device, (m, narrow), dt))
+_i32, _f32t, _u8 = torch.int32, torch.float32, torch.uint8
 
 
 def moe_w4_grouped_mm(x, w, offsets, y, stream=None):
     """y[r] <- w[e] x[r] for the rows offsets[e] <= r < offsets[e + 1] of each group.  x [M][K], w [E][N][K], y [M][N]
     bf16 or fp16; offsets int32 [E + 1].  Rows outside the groups keep what y held."""
-    _grouped("moe_w4_grouped_mm", "x", x, w, offsets, "y", y, False, stream)
+    name = "moe_w4_grouped_mm"
+    gpu, (m, k), dt = _main(name, "x", x, 2, _16BIT)
+    (e, n, _), _ = _other(name, "w", w, 3, _16BIT)
+    _enqueue(name, _lib.moe_w4_grouped_mm, gpu, stream, (
+        x.data_ptr() if x.is_contiguous() else _refuse(name, "x is not contiguous"), _arg(name, "w", w, gpu, (e, n, k), dt),
+        _arg(name, "offsets", offsets, gpu, (e + 1,), _i32), e, m, n, k, _ELEM[dt], _arg(name, "y", y, gpu, (m, n), dt)))
 
 
 def moe_w4_grouped_mm_dx(dy, w, offsets, dx, stream=None):
     """dx[r] <- w[e]^T dy[r]: the gradient of moe_w4_grouped_mm's x from dy [M][N]."""
-    _grouped("moe_w4_grouped_mm_dx", "dy", dy, w, offsets, "dx", dx, True, stream)
+    name = "moe_w4_grouped_mm_dx"
+    gpu, (m, n), dt = _main(name, "dy", dy, 2, _16BIT)
+    (e, _, k), _ = _other(name, "w", w, 3, _16BIT)
+    _enqueue(name, _lib.moe_w4_grouped_mm_dx, gpu, stream, (
+        dy.data_ptr() if dy.is_contiguous() else _refuse(name, "dy is not contiguous"), _arg(name, "w", w, gpu, (e, n, k), dt),
+        _arg(name, "offsets", offsets, gpu, (e + 1,), _i32), e, m, n, k, _ELEM[dt], _arg(name, "dx", dx, gpu, (m, k), dt)))
 
 
 def moe_w4_grouped_mm_dw(x, dy, offsets, dw, add=None, stream=None):
     """dw[e] <- add[e] + sum over the group's rows of dy[r] x[r]^T: the gradient of moe_w4_grouped_mm's w.  dw and add
     [E][N][K] of x's type or fp32; add None (0) or a tensor, dw itself among them, to add to."""
     name = "moe_w4_grouped_mm_dw"
-    device, (m, k) = _gpu(name, "x", x, 2)
-    if not isinstance(dw, torch.Tensor) or dw.dim() != 3:
-        _refuse(name, "dw is not a tensor of 3 dimensions")
-    e, n, _ = dw.shape
-    dt = (x.dtype,)
-    if x.dtype not in _16BIT or dw.dtype not in (x.dtype, torch.float32):
-        _refuse(name, f"x has type {x.dtype}, dw {dw.dtype}")
-    _enqueue(name, device, stream, _arg(name, "x", x, device, (m, k), dt), _arg(name, "dy", dy, device, (m, n), dt),
-             _arg(name, "offsets", offsets, device, (e + 1,), _I32), e, m, n, k, _ELEM[x.dtype],
-             None if add is None else _arg(name, "add", add, device, (e, n, k), (dw.dtype,)),
-             _arg(name, "dw", dw, device, (e, n, k), (dw.dtype,)), _ELEM[dw.dtype])
+    gpu, (m, k), dt = _main(name, "x", x, 2, _16BIT)
+    (e, n, _), out = _other(name, "dw", dw, 3, (dt, _f32t))
+    _enqueue(name, _lib.moe_w4_grouped_mm_dw, gpu, stream, (
+        x.data_ptr() if x.is_contiguous() else _refuse(name, "x is not contiguous"), _arg(name, "dy", dy, gpu, (m, n), dt),
+        _arg(name, "offsets", offsets, gpu, (e + 1,), _i32), e, m, n, k, _ELEM[dt],
+        None if add is None else _arg(name, "add", add, gpu, (e, n, k), out), _arg(name, "dw", dw, gpu, (e, n, k), out),
+        _ELEM[out]))
 
 
 def moe_w4_matvec_workspace_bytes(M: int, K: int) -> int:
@@ -409,33 +409,37 @@ def moe_w4_matvec(x, codes, scales, y, workspace, rotate=False, stream=None):
     (rotate: its 128-blocks are rotated first), codes uint8 [N][K / 2], scales bf16 [N][K / group], y [M][N] bf16, fp16
     or fp32; workspace: matvec_workspace(M, K)."""
     name = "moe_w4_matvec"
-    device, (m, k) = _gpu(name, "x", x, 2)
-    if not isinstance(scales, torch.Tensor) or scales.dim() != 2 or scales.shape[1] == 0 or k % scales.shape[1] != 0:
+    gpu, (m, k), dt = _main(name, "x", x, 2, _16BIT)
+    (n, groups), st = _other(name, "scales", scales, 2, _SCALES)
+    if groups == 0 or k % groups != 0:
         _refuse(name, "scales is not [N][K / group]")
-    n, groups = scales.shape
-    if not isinstance(y, torch.Tensor) or y.dtype not in _ELEM:
-        _refuse(name, "y is not a tensor of a known type")
-    _enqueue(name, device, stream, _arg(name, "x", x, device, (m, k), _16BIT),
-             _arg(name, "codes", codes, device, (n, k // 2), _U8), _arg(name, "scales", scales, device, (n, groups), _SCALES),
-             m, n, k, k // groups, 1 if rotate else 0, _ELEM[x.dtype], _arg(name, "y", y, device, (m, n), (y.dtype,)),
-             _ELEM[y.dtype], _arg(name, "workspace", workspace, device, workspace.shape, _U8), workspace.numel())
+    _, out = _other(name, "y", y, 2, _ANY)
+    (room,), _ = _other(name, "workspace", workspace, 1, (_u8,))
+    _enqueue(name, _lib.moe_w4_matvec, gpu, stream, (
+        x.data_ptr() if x.is_contiguous() else _refuse(name, "x is not contiguous"),
+        _arg(name, "codes", codes, gpu, (n, k // 2), _u8), _arg(name, "scales", scales, gpu, (n, groups), st), m, n, k,
+        k // groups, 1 if rotate else 0, _ELEM[dt], _arg(name, "y", y, gpu, (m, n), out), _ELEM[out],
+        _arg(name, "workspace", workspace, gpu, (room,), _u8), room))
 
 
-def _norm_inputs(name, resid, y, gate, gate_kind, post_norm, pre_norm, post_gain, pre_gain, dtype):
-    """Addresses of the inputs that the two passes share, and their types."""
-    device, (t, h) = _gpu(name, "resid", resid, 2)
-    if dtype not in _ELEM or resid.dtype not in (dtype, torch.float32):
-        _refuse(name, f"types {dtype} and {resid.dtype} of the residual stream")
-    dt = (dtype,)
-    shapes = {GATE_TOKEN: (t,), GATE_CHANNEL: (h,), GATE_FULL: (t, h)}
-    if (gate is None) != (gate_kind == GATE_NONE) or gate_kind not in (GATE_NONE, *shapes):
-        _refuse(name, "gate and gate_kind do not fit")
-    flags = (NORM_POST if post_norm else 0) | (NORM_PRE if pre_norm else 0)
-    return (device, t, h, dt, flags, _arg(name, "resid", resid, device, (t, h), (resid.dtype,)),
-            None if y is None else _arg(name, "y", y, device, (t, h), dt),
-            None if gate is None else _arg(name, "gate", gate, device, shapes[gate_kind], dt),
-            None if post_gain is None else _arg(name, "post_gain", post_gain, device, (h,), dt),
-            None if pre_gain is None else _arg(name, "pre_gain", pre_gain, device, (h,), dt))
+def _norm_form(name, resid, like, gate, gate_kind, post_gain, pre_gain, post_norm, pre_norm):
+    """What the two passes check alike: GPU, sizes, types, flags and the addresses of gate and gains."""
+    gpu, (t, h), rt = _main(name, "resid", resid, 2, _ANY)
+    _, dt = _other(name, "y (or x)", like, 2, _ANY)
+    if rt is not dt and rt is not _f32t:
+        _refuse(name, f"types {dt} and {rt} of the residual stream")
+    if gate is None:
+        if gate_kind != GATE_NONE:
+            _refuse(name, "gate_kind without a gate")
+        p_gate = None
+    else:
+        shape = (t,) if gate_kind == GATE_TOKEN else (h,) if gate_kind == GATE_CHANNEL else (t, h) if gate_kind == GATE_FULL else None
+        if shape is None:
+            _refuse(name, "a gate without its gate_kind")
+        p_gate = _arg(name, "gate", gate, gpu, shape, dt)
+    return (gpu, t, h, dt, rt, (NORM_POST if post_norm else 0) | (NORM_PRE if pre_norm else 0), p_gate,
+            None if post_gain is None else _arg(name, "post_gain", post_gain, gpu, (h,), dt),
+            None if pre_gain is None else _arg(name, "pre_gain", pre_gain, gpu, (h,), dt))
 
 
 def moe_w4_norm_residual(resid, y, resid_out, x_out, gate=None, gate_kind=GATE_NONE, scale=1.0, post_norm=False,
@@ -443,15 +447,14 @@ def moe_w4_norm_residual(resid, y, resid_out, x_out, gate=None, gate_kind=GATE_N
     """resid_out <- resid + scale * gate * (norm of) y, x_out <- its norm times pre_gain, over rows [T][H].  y None:
     x_out <- norm(resid) alone (resid_out None); pre_norm False: x_out None."""
     name = "moe_w4_norm_residual"
-    like = y if y is not None else x_out
-    if not isinstance(like, torch.Tensor):
-        _refuse(name, "neither y nor x_out is a tensor")
-    device, t, h, dt, flags, p_resid, p_y, p_gate, p_post, p_pre = _norm_inputs(
-        name, resid, y, gate, gate_kind, post_norm, pre_norm, post_gain, pre_gain, like.dtype)
-    _enqueue(name, device, stream, p_resid, p_y, p_gate, gate_kind, scale, p_post, p_pre, flags, eps, t, h,
-             _ELEM[like.dtype], _ELEM[resid.dtype],
-             None if resid_out is None else _arg(name, "resid_out", resid_out, device, (t, h), (resid.dtype,)),
-             None if x_out is None else _arg(name, "x_out", x_out, device, (t, h), dt))
+    gpu, t, h, dt, rt, flags, p_gate, p_post, p_pre = _norm_form(
+        name, resid, x_out if y is None else y, gate, gate_kind, post_gain, pre_gain, post_norm, pre_norm)
+    shape = (t, h)
+    _enqueue(name, _lib.moe_w4_norm_residual, gpu, stream, (
+        resid.data_ptr() if resid.is_contiguous() else _refuse(name, "resid is not contiguous"),
+        None if y is None else _arg(name, "y", y, gpu, shape, dt), p_gate, gate_kind, scale, p_post, p_pre, flags, eps, t, h,
+        _ELEM[dt], _ELEM[rt], None if resid_out is None else _arg(name, "resid_out", resid_out, gpu, shape, rt),
+        None if x_out is None else _arg(name, "x_out", x_out, gpu, shape, dt)))
 
 
 def moe_w4_norm_workspace_bytes(T: int, H: int) -> int:
@@ -465,25 +468,22 @@ def moe_w4_norm_residual_backward(resid_out, y, d_resid_out, d_x, d_resid, d_y, 
     where given d_gate (fp32 for a token's or channel's gate, y's type for a full one), d_post_gain and d_pre_gain
     (fp32 [H]).  resid_out: the stream that the forward pass wrote; workspace: norm_workspace(T, H)."""
     name = "moe_w4_norm_residual_backward"
-    like = y if y is not None else d_x
-    if not isinstance(like, torch.Tensor):
-        _refuse(name, "neither y nor d_x is a tensor")
-    device, t, h, dt, flags, p_resid, p_y, p_gate, p_post, p_pre = _norm_inputs(
-        name, resid_out, y, gate, gate_kind, post_norm, pre_norm, post_gain, pre_gain, like.dtype)
-    rt = (resid_out.dtype,)
+    gpu, t, h, dt, rt, flags, p_gate, p_post, p_pre = _norm_form(
+        name, resid_out, d_x if y is None else y, gate, gate_kind, post_gain, pre_gain, post_norm, pre_norm)
     if d_gate is not None and gate is None:
         _refuse(name, "d_gate without a gate")
-    _enqueue(name, device, stream, p_resid, p_y, p_gate, gate_kind, scale, p_post, p_pre, flags, eps, t, h,
-             _ELEM[like.dtype], _ELEM[resid_out.dtype],
-             None if d_resid_out is None else _arg(name, "d_resid_out", d_resid_out, device, (t, h), rt),
-             None if d_x is None else _arg(name, "d_x", d_x, device, (t, h), dt),
-             _arg(name, "d_resid", d_resid, device, (t, h), rt),
-             None if d_y is None else _arg(name, "d_y", d_y, device, (t, h), dt),
-             None if d_gate is None else _arg(name, "d_gate", d_gate, device, gate.shape,
-                                              dt if gate_kind == GATE_FULL else _F32),
-             None if d_post_gain is None else _arg(name, "d_post_gain", d_post_gain, device, (h,), _F32),
-             None if d_pre_gain is None else _arg(name, "d_pre_gain", d_pre_gain, device, (h,), _F32),
-             _arg(name, "workspace", workspace, device, workspace.shape, _U8), workspace.numel())
+    shape = (t, h)
+    (room,), _ = _other(name, "workspace", workspace, 1, (_u8,))
+    _enqueue(name, _lib.moe_w4_norm_residual_backward, gpu, stream, (
+        resid_out.data_ptr() if resid_out.is_contiguous() else _refuse(name, "resid_out is not contiguous"),
+        None if y is None else _arg(name, "y", y, gpu, shape, dt), p_gate, gate_kind, scale, p_post, p_pre, flags, eps, t, h,
+        _ELEM[dt], _ELEM[rt], None if d_resid_out is None else _arg(name, "d_resid_out", d_resid_out, gpu, shape, rt),
+        None if d_x is None else _arg(name, "d_x", d_x, gpu, shape, dt), _arg(name, "d_resid", d_resid, gpu, shape, rt),
+        None if d_y is None else _arg(name, "d_y", d_y, gpu, shape, dt),
+        None if d_gate is None else _arg(name, "d_gate", d_gate, gpu, gate.shape, dt if gate_kind == GATE_FULL else _f32t),
+        None if d_post_gain is None else _arg(name, "d_post_gain", d_post_gain, gpu, (h,), _f32t),
+        None if d_pre_gain is None else _arg(name, "d_pre_gain", d_pre_gain, gpu, (h,), _f32t),
+        _arg(name, "workspace", workspace, gpu, (room,), _u8), room))
 
 
 def moe_w4_set_fused_wait(max_ticks: int = 0, extra_count: int = 0):
