@@ -381,6 +381,10 @@ int moe_w4_dense_mlp(const void *x, const void *w, int64_t T, void *y, void *wor
  * Offsets ascend within [0, M].  They are read on the device only: values
  * outside are taken as the nearest of [0, M], a group that would end before it
  * begins is empty, and rows claimed by two groups hold either's result.
+ * dw's workspace: at least moe_w4_grouped_mm_dw_workspace_bytes() bytes (0 for
+ * most sizes), contents on entry irrelevant, or NULL: with it, few groups of many
+ * rows are summed in slices that are added in order, in fp32 (1 x 65536 rows, 512 x
+ * 512: 48 us against 629); without, in one run.  EWORKSPACE for a shorter one.
  * The results of a call depend on its arguments only (no atomics).
  * N, K: multiples of 8, 8 .. MOE_W4_GROUPED_MAX_DIM; M: 0 ..
  * MOE_W4_GROUPED_MAX_ROWS; n_groups: 0 .. MOE_W4_GROUPED_MAX_GROUPS (0: nothing
@@ -394,7 +398,9 @@ int moe_w4_grouped_mm(const void *x, const void *w, const int32_t *offsets, int6
 int moe_w4_grouped_mm_dx(const void *dy, const void *w, const int32_t *offsets, int64_t n_groups, int64_t M, int64_t N,
                          int64_t K, int dtype, void *dx, void *stream);
 int moe_w4_grouped_mm_dw(const void *x, const void *dy, const int32_t *offsets, int64_t n_groups, int64_t M, int64_t N,
-                         int64_t K, int dtype, const void *add, void *dw, int dw_dtype, void *stream);
+                         int64_t K, int dtype, const void *add, void *dw, int dw_dtype, void *workspace,
+                         size_t workspace_bytes, void *stream);
+size_t moe_w4_grouped_mm_dw_workspace_bytes(int64_t n_groups, int64_t M, int64_t N, int64_t K);   /* (0 also for sizes out of range) */
 
 /* Products of 4-bit weight rows with 1 .. MOE_W4_MATVEC_MAX_TOKENS tokens, the
  * decode form of a linear in the experts' container format:

@@ -860,19 +860,28 @@ int moe_w4_grouped_mm_dx(const void *dy, const void *w, const int32_t *offsets, 
     return device_status(hipGetLastError());
 }
 
+size_t moe_w4_grouped_mm_dw_workspace_bytes(int64_t n_groups, int64_t M, int64_t N, int64_t K) {
+    if (!grouped_sizes_ok(n_groups, M, N, K, MOE_W4_BF16) || n_groups == 0) return 0;
+    const int slices = grouped_dw_slices((int)n_groups, (int)M, (int)N, (int)K);
+    return slices > 1 ? (size_t)(n_groups * N * K) * slices * 4 : 0;
+}
+
 int moe_w4_grouped_mm_dw(const void *x, const void *dy, const int32_t *offsets, int64_t n_groups, int64_t M, int64_t N,
-                         int64_t K, int dtype, const void *add, void *dw, int dw_dtype, void *stream) {
+                         int64_t K, int dtype, const void *add, void *dw, int dw_dtype, void *workspace,
+                         size_t workspace_bytes, void *stream) {
     if (!grouped_sizes_ok(n_groups, M, N, K, dtype) || (dw_dtype != dtype && dw_dtype != MOE_W4_F32)) return MOE_W4_EINVAL;
     if (n_groups == 0) return MOE_W4_OK;
     if (!offsets || !dw || (M > 0 && (!x || !dy))) return MOE_W4_EINVAL;   // M == 0: dw is add, or zeros
     const size_t nw = (size_t)(n_groups * N * K) * elem_bytes(dw_dtype);
     const Span in[] = {{M > 0 ? x : nullptr, (size_t)(M * K) * 2, 16}, {M > 0 ? dy : nullptr, (size_t)(M * N) * 2, 16},
                        {offsets, (size_t)(n_groups + 1) * 4, 4}, {add == dw ? nullptr : add, nw, 16}};
-    const Span out[] = {{dw, nw, 16}};
-    if (!all_aligned(in) || !all_aligned(out) || !outputs_apart(in, out)) return MOE_W4_EINVAL;
+    const Span out[] = {{dw, nw, 16}, {workspace, workspace_bytes, 16}};
+    if (!all_aligned(in) || !all_aligned(out)) return MOE_W4_EINVAL;
+    if (workspace && workspace_bytes < moe_w4_grouped_mm_dw_workspace_bytes(n_groups, M, N, K)) return MOE_W4_EWORKSPACE;
+    if (!outputs_apart(in, out)) return MOE_W4_EINVAL;
     (void)hipGetLastError();
     launch_grouped_mm_dw(x, dy, offsets, (int)n_groups, (int)M, (int)N, (int)K, dtype == MOE_W4_BF16,
-                         dw_dtype == MOE_W4_F32, add, dw, static_cast<hipStream_t>(stream));
+                         dw_dtype == MOE_W4_F32, add, dw, static_cast<float *>(workspace), static_cast<hipStream_t>(stream));
     return device_status(hipGetLastError());
 }
 

@@ -40,6 +40,7 @@ struct GroupedArgs {
     const void *add;          // dw: added to the sums, or null
     int groups, rows;
     int n, k;
+    int slices;               // dw: parts that each group's rows are split into (groups counts the parts)
 };
 
 namespace {
@@ -239,7 +240,13 @@ __device__ __forceinline__ Range survey(const GroupedArgs &g, int tiles_m, int t
     auto weight = [&](int rows) { return (rows + kStep - 1) / kStep + kTileFixed; };   // dw: of each tile of the group
     int tiles = 0, work = 0;
     for (int e = e0; e < e1; ++e) {
-        const int lo = min(max(g.offsets[e], 0), g.rows), hi = min(max(g.offsets[e + 1], lo), g.rows);
+        const int of = MODE == kDw ? e / g.slices : e;
+        int lo = min(max(g.offsets[of], 0), g.rows), hi = min(max(g.offsets[of + 1], lo), g.rows);
+        if (MODE == kDw && g.slices > 1) {   // slice e % slices, of whole steps
+            const int each = ((hi - lo + kStep - 1) / kStep + g.slices - 1) / g.slices * kStep;
+            lo = min(lo + e % g.slices * each, hi);
+            hi = min(lo + each, hi);
+        }
         first[e] = lo;
         count[e] = hi - lo;
         tiles += tiles_of(hi - lo);
@@ -583,38 +590,97 @@ static void launch_rows(const GroupedArgs &g, hipStream_t s) {
         launch_tile<MODE, BF16, false, 128, 128, 2, 2, 2>(g, s);
 }
 
+// out[i] = add[i] + the sum of the slices' [i] in order, 8 elements a thread.
+template <bool BF16, bool F32OUT>
+__global__ __launch_bounds__(256) void k_grouped_join(const float *parts, int slices, int64_t each, int64_t all, const void *add,
+                                                      void *out) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
+    if (i >= all) return;
+    const float *p = parts + i / each * slices * each + i % each;   // each: one group's elements, a multiple of 64
+    f32x4_t a = {0.0f, 0.0f, 0.0f, 0.0f}, b = a;
+#pragma unroll 4
+    for (int s = 0; s < slices; ++s) {
+        a += *reinterpret_cast<const f32x4_t *>(p + s * each);
+        b += *reinterpret_cast<const f32x4_t *>(p + s * each + 4);
+    }
+    if constexpr (F32OUT) {
+        if (add) {
+            a += *reinterpret_cast<const f32x4_t *>(static_cast<const float *>(add) + i);
+            b += *reinterpret_cast<const f32x4_t *>(static_cast<const float *>(add) + i + 4);
+        }
+        *reinterpret_cast<f32x4_t *>(static_cast<float *>(out) + i) = a;
+        *reinterpret_cast<f32x4_t *>(static_cast<float *>(out) + i + 4) = b;
+    } else {
+        if (add) {
+            const uint4 o = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(add) + i);
+            const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                (k < 2 ? a : b)[2 * (k & 1)] += widen16<BF16>((uint16_t)w[k]);
+                (k < 2 ? a : b)[2 * (k & 1) + 1] += widen16<BF16>((uint16_t)(w[k] >> 16));
+            }
+        }
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(out) + i) = make_uint4(
+            pack16<BF16>(a[0], a[1]), pack16<BF16>(a[2], a[3]), pack16<BF16>(b[0], b[1]), pack16<BF16>(b[2], b[3]));
+    }
+}
+
+// dw of few tiles and many rows: the rows of each group in this many slices, so
+// that about two workgroups a CU have work, of at least 16 steps each on average (1 x
+// 65536 rows, 512 x 512: 48 us against 629; of 8 steps, 4 x 2000 rows: 26 against 23);
+// the slices' sums go to the workspace in fp32 and are joined by a second launch.
+int grouped_dw_slices(int groups, int rows, int n, int k) {
+    const int64_t tiles = (int64_t)groups * ((n + 127) / 128) * ((k + 127) / 128);
+    const int64_t fill = 2 * kCus / tiles, steps = (int64_t)rows / groups / (16 * kStep);
+    const int64_t s = fill < steps ? fill : steps;
+    return s > 1 ? (int)s : 1;
+}
+
 // dw: large tiles for many of them with many rows to sum over (256 groups x 384
 // rows, 1024 x 2048: 1090 us against 1295); else twice the workgroups, whose
 // stores and products overlap (256 x 48 rows: 930 against 981; 1 x 65536 rows,
 // 2048 x 2048, 64 large tiles: 846 against 1488).
 template <bool BF16, bool F32OUT>
-static void launch_dw(const GroupedArgs &g, hipStream_t s) {
+static void launch_dw(const GroupedArgs &g, float *parts, hipStream_t s) {
     const int64_t tiles = (int64_t)g.groups * ((g.n + 255) / 256) * ((g.k + 255) / 256);
-    if (tiles >= 2048 && g.rows / g.groups >= kMinRows)
+    const int slices = parts ? grouped_dw_slices(g.groups, g.rows, g.n, g.k) : 1;
+    if (slices > 1) {
+        GroupedArgs h = g;
+        h.groups = g.groups * slices;
+        h.slices = slices;
+        h.out = parts;
+        h.add = nullptr;
+        launch_tile<kDw, BF16, true, 128, 128, 2, 2, 2>(h, s);
+        if (hipPeekAtLastError() != hipSuccess) return;
+        const int64_t each = (int64_t)g.n * g.k, all = each * g.groups;
+        hipLaunchKernelGGL((k_grouped_join<BF16, F32OUT>), dim3((unsigned)((all + 2047) / 2048)), dim3(256), 0, s, parts, slices, each,
+                           all, g.add, g.out);
+    } else if (tiles >= 2048 && g.rows / g.groups >= kMinRows) {
         launch_tile<kDw, BF16, F32OUT, 256, 256, 2, 4, 2>(g, s);
-    else
+    } else {
         launch_tile<kDw, BF16, F32OUT, 128, 128, 2, 2, 2>(g, s);
+    }
 }
 
 void launch_grouped_mm(const void *x, const void *w, const int *offsets, int groups, int rows, int n, int k, bool bf16,
                        void *y, hipStream_t s) {
-    const GroupedArgs g{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(w), offsets, y, nullptr, groups, rows, n, k};
+    const GroupedArgs g{static_cast<const uint8_t *>(x), static_cast<const uint8_t *>(w), offsets, y, nullptr, groups, rows, n, k, 1};
     if (bf16) launch_rows<kMm, true>(g, s); else launch_rows<kMm, false>(g, s);
 }
 
 void launch_grouped_mm_dx(const void *dy, const void *w, const int *offsets, int groups, int rows, int n, int k, bool bf16,
                           void *dx, hipStream_t s) {
-    const GroupedArgs g{static_cast<const uint8_t *>(dy), static_cast<const uint8_t *>(w), offsets, dx, nullptr, groups, rows, n, k};
+    const GroupedArgs g{static_cast<const uint8_t *>(dy), static_cast<const uint8_t *>(w), offsets, dx, nullptr, groups, rows, n, k, 1};
     if (bf16) launch_rows<kDx, true>(g, s); else launch_rows<kDx, false>(g, s);
 }
 
 void launch_grouped_mm_dw(const void *x, const void *dy, const int *offsets, int groups, int rows, int n, int k, bool bf16,
-                          bool f32_out, const void *add, void *dw, hipStream_t s) {
-    const GroupedArgs g{static_cast<const uint8_t *>(dy), static_cast<const uint8_t *>(x), offsets, dw, add, groups, rows, n, k};
+                          bool f32_out, const void *add, void *dw, float *parts, hipStream_t s) {
+    const GroupedArgs g{static_cast<const uint8_t *>(dy), static_cast<const uint8_t *>(x), offsets, dw, add, groups, rows, n, k, 1};
     if (bf16) {
-        if (f32_out) launch_dw<true, true>(g, s); else launch_dw<true, false>(g, s);
+        if (f32_out) launch_dw<true, true>(g, parts, s); else launch_dw<true, false>(g, parts, s);
     } else {
-        if (f32_out) launch_dw<false, true>(g, s); else launch_dw<false, false>(g, s);
+        if (f32_out) launch_dw<false, true>(g, parts, s); else launch_dw<false, false>(g, parts, s);
     }
 }
 

@@ -211,7 +211,9 @@ void launch_grouped_mm(const void *x, const void *w, const int *offsets, int gro
 void launch_grouped_mm_dx(const void *dy, const void *w, const int *offsets, int groups, int rows, int n, int k, bool bf16,
                           void *dx, hipStream_t s);
 void launch_grouped_mm_dw(const void *x, const void *dy, const int *offsets, int groups, int rows, int n, int k, bool bf16,
-                          bool f32_out, const void *add, void *dw, hipStream_t s);
+                          bool f32_out, const void *add, void *dw, float *parts, hipStream_t s);
+// parts: fp32 [groups * slices][n][k] for the slices that the rows are split into, or null (no split)
+int grouped_dw_slices(int groups, int rows, int n, int k);
 
 // The norms around a block with its gate and residual scale (norm.hip).
 enum GateKind { kGateNone = 0, kGateToken = 1, kGateChannel = 2, kGateFull = 3 };

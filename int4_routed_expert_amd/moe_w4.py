@@ -100,7 +100,8 @@ _sig = {
     "moe_w4_generate_normal_bf16": (_int, [_u64, ctypes.c_uint32, _i64, ctypes.c_double, _vp, _vp]),
     "moe_w4_grouped_mm": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp, _vp]),
     "moe_w4_grouped_mm_dx": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp, _vp]),
-    "moe_w4_grouped_mm_dw": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp, _vp, _int, _vp]),
+    "moe_w4_grouped_mm_dw": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _i64, _int, _vp, _vp, _int, _vp, _sz, _vp]),
+    "moe_w4_grouped_mm_dw_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64]),
     "moe_w4_matvec_workspace_bytes": (_sz, [_i64, _i64]),
     "moe_w4_matvec": (_int, [_vp, _vp, _vp, _i64, _i64, _i64, _int, _int, _int, _vp, _int, _vp, _sz, _vp]),
     "moe_w4_norm_residual": (_int, [_vp, _vp, _vp, _int, _f32, _vp, _vp, _int, _f32, _i64, _i64, _int, _int, _vp, _vp,
@@ -387,17 +388,31 @@ def moe_w4_grouped_mm_dx(dy, w, offsets, dx, stream=None):
         _arg(name, "offsets", offsets, gpu, (e + 1,), _i32), e, m, n, k, _ELEM[dt], _arg(name, "dx", dx, gpu, (m, k), dt)))
 
 
-def moe_w4_grouped_mm_dw(x, dy, offsets, dw, add=None, stream=None):
+def moe_w4_grouped_mm_dw_workspace_bytes(n_groups: int, M: int, N: int, K: int) -> int:
+    return _lib.moe_w4_grouped_mm_dw_workspace_bytes(n_groups, M, N, K)
+
+
+def moe_w4_grouped_mm_dw(x, dy, offsets, dw, add=None, workspace=None, stream=None):
     """dw[e] <- add[e] + sum over the group's rows of dy[r] x[r]^T: the gradient of moe_w4_grouped_mm's w.  dw and add
-    [E][N][K] of x's type or fp32; add None (0) or a tensor, dw itself among them, to add to."""
+    [E][N][K] of x's type or fp32; add None (0) or a tensor, dw itself among them, to add to.  workspace: uint8 of
+    moe_w4_grouped_mm_dw_workspace_bytes, or None: taken from PyTorch's allocator for the call, where it is needed."""
     name = "moe_w4_grouped_mm_dw"
     gpu, (m, k), dt = _main(name, "x", x, 2, _16BIT)
     (e, n, _), out = _other(name, "dw", dw, 3, (dt, _f32t))
+    room = 0
+    if workspace is None:
+        room = _lib.moe_w4_grouped_mm_dw_workspace_bytes(e, m, n, k)
+        if room:
+            workspace = torch.empty((room,), dtype=_u8, device=x.device)
+            if stream is not None:   # the allocator must know of a stream other than the current one
+                workspace.record_stream(torch.cuda.ExternalStream(stream, x.device) if isinstance(stream, int) else stream)
+    else:
+        (room,), _ = _other(name, "workspace", workspace, 1, (_u8,))
     _enqueue(name, _lib.moe_w4_grouped_mm_dw, gpu, stream, (
         x.data_ptr() if x.is_contiguous() else _refuse(name, "x is not contiguous"), _arg(name, "dy", dy, gpu, (m, n), dt),
         _arg(name, "offsets", offsets, gpu, (e + 1,), _i32), e, m, n, k, _ELEM[dt],
         None if add is None else _arg(name, "add", add, gpu, (e, n, k), out), _arg(name, "dw", dw, gpu, (e, n, k), out),
-        _ELEM[out]))
+        _ELEM[out], None if workspace is None else _arg(name, "workspace", workspace, gpu, (room,), _u8), room))
 
 
 def moe_w4_matvec_workspace_bytes(M: int, K: int) -> int:

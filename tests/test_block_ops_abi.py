@@ -46,10 +46,14 @@ def test_grouped_rows(m, which):
 
 
 def test_grouped_dw(m):
-    def call(x=X, dy=W, off=OFF, e=4, M=100, N=64, K=128, dt=m.F16, add=None, dw=Y, dwt=m.F32):
-        return m._lib.moe_w4_grouped_mm_dw(x, dy, off, e, M, N, K, dt, add, dw, dwt, None)
+    def call(x=X, dy=W, off=OFF, e=4, M=100, N=64, K=128, dt=m.F16, add=None, dw=Y, dwt=m.F32, ws=None, nb=0):
+        return m._lib.moe_w4_grouped_mm_dw(x, dy, off, e, M, N, K, dt, add, dw, dwt, ws, nb, None)
 
     E = m.EINVAL
+    big = m.moe_w4_grouped_mm_dw_workspace_bytes(1, 65536, 64, 128)
+    assert big >= 2 * 64 * 128 * 4 and m.moe_w4_grouped_mm_dw_workspace_bytes(256, 65536, 1024, 2048) == 0
+    assert m.moe_w4_grouped_mm_dw_workspace_bytes(1, 65536, 60, 128) == 0 and m.moe_w4_grouped_mm_dw_workspace_bytes(0, 9, 64, 128) == 0
+    table(call, {"e": 1, "M": 65536}, [({"ws": WS, "nb": big - 1}, m.EWORKSPACE), ({"ws": WS + 8, "nb": big}, E), ({"ws": Y, "nb": big}, E)])
     table(call, {}, [({"e": 0}, m.OK), ({"M": -1}, E), ({"N": 4}, E), ({"dt": m.F32}, E), ({"dwt": m.BF16}, E), ({"dwt": 9}, E),
                      ({"x": None}, E), ({"dy": None}, E), ({"off": None}, E), ({"dw": None}, E), ({"M": 0, "dw": None}, E),
                      ({"x": X + 8}, E), ({"dw": Y + 4}, E), ({"add": WS + 4}, E), ({"dw": X}, E), ({"dw": W + 256}, E),

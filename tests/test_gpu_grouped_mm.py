@@ -133,6 +133,32 @@ def test_dw_adds_in_its_own_type(m, dtype):
         check(out[e], ref, mag, b - a + 1, dtype, f"group {e}")
 
 
+@pytest.mark.parametrize("counts,n,k", [([30000], 72, 136), ([9000, 0, 700, 12001], 264, 40), ([1, 0, 40000], 8, 8)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_dw_in_slices(m, counts, n, k, dtype):
+    """Few groups of many rows: summed in slices that a second launch joins; with and without a workspace given."""
+    off, x, dy, w = make(counts, n, k, dtype, 17, behind=9)
+    offsets, x, dy = torch.from_numpy(off).cuda(), x.cuda(), dy.cuda()
+    nb = m.moe_w4_grouped_mm_dw_workspace_bytes(len(counts), x.shape[0], n, k)
+    assert nb > 0
+    ws = torch.full((nb,), 0xFF, dtype=torch.uint8, device="cuda")
+    add = torch.randn(w.shape, device="cuda")
+    full, half, own = (torch.full(w.shape, 7.0, dtype=t, device="cuda") for t in (torch.float32, DT[dtype], torch.float32))
+    m.moe_w4_grouped_mm_dw(x, dy, offsets, full, add=add, workspace=ws)
+    m.moe_w4_grouped_mm_dw(x, dy, offsets, half, add=w.cuda(), workspace=ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    m.moe_w4_grouped_mm_dw(x, dy, offsets, own, add=add, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(own, full)
+    for e in range(len(counts)):
+        a, b = int(off[e]), int(off[e + 1])
+        ref, mag = dy[a:b].double().t() @ x[a:b].double(), dy[a:b].double().abs().t() @ x[a:b].double().abs()
+        check(full[e], (ref + add[e].double()).cpu(), (mag + add[e].double().abs()).cpu(), b - a + 1, "f32", f"group {e}")
+        W = w[e].double()
+        check(half[e], ref.cpu() + W, mag.cpu() + W.abs(), b - a + 1, dtype, f"16-bit group {e}")
+
+
 def test_no_rows_at_all(m):
     offsets = torch.zeros(4, dtype=torch.int32, device="cuda")
     x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
