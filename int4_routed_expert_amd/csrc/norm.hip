@@ -180,20 +180,56 @@ __global__ __launch_bounds__(64 * WAVES *ROWS) void k_norm(NormArgs a) {
     }
 }
 
-// Column sums of the rows of one workgroup slice go to parts[which][slice][H].
-template <int ACT, int RES, int WAVES, int V, int ROWS>
+// Backward.  With w = scale * post_gain * (channel gate) of a column, e = d r * n
+// and the gate of the row or element g (1 otherwise), all that depends on y is
+//   k = g w d r,    d gate = w e   (full: stored; token: summed over the row,
+//   which is also sum(k n) / g),
+// and both d post_gain and the channel gate's gradient are a constant of the column
+// times Q = sum_t g e: one sum in registers serves the two, and one more d pre_gain.
+// Column sums of a workgroup's rows go to parts[which][workgroup][H].
+template <int ACT, int RES, int WAVES, int V, int ROWS, int KIND>   // KIND: kGateToken, kGateFull, or kGateChannel (none too)
 __global__ __launch_bounds__(64 * WAVES *ROWS) void k_norm_back(NormBackArgs a) {
     __shared__ float red[3][ROWS][3 * WAVES];   // first sums of even and odd rounds, second sums
     const int wave = (threadIdx.x >> 6) % WAVES, sub = (threadIdx.x >> 6) / WAVES;
     const int c0 = (wave * 64 + (threadIdx.x & 63)) * 8;
     const bool post = a.flags & kNormPost, pre = a.flags & kNormPre;
     const int slice = blockIdx.x * ROWS + sub, slices = gridDim.x * ROWS;
-    float s_pre[V][8], s_post[V][8], s_gate[V][8];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s_pre[v][i] = s_post[v][i] = s_gate[v][i] = 0.0f;
     const float inv_h = 1.0f / (float)a.H;
+    float s_pre[V][8], s_q[V][8];
+    auto gain = [&](int v, float (&b)[8]) {   // pre_gain of this lane's columns
+        const int c = c0 + v * WAVES * 512;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) b[i] = 1.0f;
+        if (c < a.H && a.pre_gain) load8<ACT>(a.pre_gain, c, b);
+    };
+    auto weight = [&](int v, float (&w)[8]) {
+        const int c = c0 + v * WAVES * 512;
+        float g[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = a.scale, g[i] = 1.0f;
+        if (c >= a.H) return;
+        if (a.post_gain) load8<ACT>(a.post_gain, c, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] *= g[i];
+        if (KIND == kGateChannel && a.gate) {
+            load8<ACT>(a.gate, c, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] *= g[i];
+        }
+    };
+    // both held over the rows, but in workgroups of 16 waves, whose registers they
+    // would overflow (4000 x 8192: 137 us so, 162 held and spilled)
+    constexpr bool kHold = WAVES < 16;
+    float held_b[kHold ? V : 1][8], held_w[kHold ? V : 1][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s_pre[v][i] = s_q[v][i] = 0.0f;
+        if constexpr (kHold) {
+            gain(v, held_b[v]);
+            weight(v, held_w[v]);
+        }
+    }
     // every row of a workgroup runs as many rounds, so that all meet at the barriers
     const int64_t rounds = (a.T + slices - 1) / slices;
     for (int64_t n = 0; n < rounds; ++n) {
@@ -202,30 +238,31 @@ __global__ __launch_bounds__(64 * WAVES *ROWS) void k_norm_back(NormBackArgs a) 
         const size_t at = (size_t)(live ? row : 0) * a.H;
         float r[V][8], y[V][8], dr[V][8], dx[V][8];
         bool in[V];
+        float sums[3] = {0.0f, 0.0f, 0.0f};   // r'^2, h r', y^2
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int c = c0 + v * WAVES * 512;
             in[v] = live && c < a.H;
 #pragma unroll
             for (int i = 0; i < 8; ++i) r[v][i] = y[v][i] = dr[v][i] = dx[v][i] = 0.0f;
-            if (in[v]) {
-                if (pre) {
-                    load8<RES>(a.resid_out, at + c, r[v]);
-                    load8<ACT>(a.d_x, at + c, dx[v]);
-                }
-                if (a.y) load8<ACT>(a.y, at + c, y[v]);
-                if (a.d_resid_out) load8<RES>(a.d_resid_out, at + c, dr[v]);
+            if (!in[v]) continue;
+            if (pre) {
+                load8<RES>(a.resid_out, at + c, r[v]);
+                load8<ACT>(a.d_x, at + c, dx[v]);
             }
+            if (a.y) load8<ACT>(a.y, at + c, y[v]);
+            if (a.d_resid_out) load8<RES>(a.d_resid_out, at + c, dr[v]);
         }
-        float sums[3] = {0.0f, 0.0f, 0.0f};   // r'^2, h r', y^2
+        const float tok = KIND == kGateToken && live ? load1<ACT>(a.gate, (size_t)row) : 1.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            float g[8];
-            if (pre && a.pre_gain && in[v]) load8<ACT>(a.pre_gain, c0 + v * WAVES * 512, g);
+            float own[8];
+            if constexpr (!kHold) gain(v, own);
+            const float(&b)[8] = kHold ? held_b[kHold ? v : 0] : own;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 sums[0] += r[v][i] * r[v][i];
-                sums[1] += (a.pre_gain && in[v] && pre ? g[i] * dx[v][i] : dx[v][i]) * r[v][i];
+                sums[1] += b[i] * dx[v][i] * r[v][i];
                 sums[2] += y[v][i] * y[v][i];
             }
         }
@@ -233,74 +270,102 @@ __global__ __launch_bounds__(64 * WAVES *ROWS) void k_norm_back(NormBackArgs a) 
         const float q = pre ? 1.0f / sqrtf(sums[0] * inv_h + a.eps) : 0.0f;
         const float m = q * q * sums[1] * inv_h;   // mean(h u) q
         const float p = post ? 1.0f / sqrtf(sums[2] * inv_h + a.eps) : 1.0f;
-        const float tok = a.gate_kind == kGateToken && live ? load1<ACT>(a.gate, (size_t)row) : 1.0f;
-        float rs[2] = {0.0f, 0.0f};   // k n, d r s
+        float kn[1] = {0.0f};   // sum of w d r n (full gate: of k n)
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             if (!in[v]) continue;
             const int c = c0 + v * WAVES * 512;
-            float t[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s_pre[v][i] += dx[v][i] * r[v][i] * q;
-            if (pre && a.pre_gain) {
-                load8<ACT>(a.pre_gain, c, t);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dx[v][i] *= t[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dr[v][i] += q * (dx[v][i] - r[v][i] * m);
-            store8<RES>(a.d_resid, at + c, dr[v]);
-            if (!a.y) continue;
-            // from here on r: s / post_gain's n, dx: k
-            float g[8], pg[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = tok, pg[i] = 1.0f;
-            if (a.gate_kind >= kGateChannel) load8<ACT>(a.gate, a.gate_kind == kGateFull ? at + c : (size_t)c, g);
-            if (a.post_gain) load8<ACT>(a.post_gain, c, pg);
+            float own[8];
+            if constexpr (!kHold) gain(v, own);
+            const float(&b)[8] = kHold ? held_b[kHold ? v : 0] : own;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float nn = y[v][i] * p, d = a.scale * dr[v][i], ds = d * g[i];
-                r[v][i] = nn;
-                dx[v][i] = ds * pg[i];
-                t[i] = d * nn * pg[i];   // d gate
-                s_post[v][i] += ds * nn;
-                s_gate[v][i] += t[i];
-                rs[0] += dx[v][i] * nn;
-                rs[1] += t[i];
+                s_pre[v][i] += dx[v][i] * (r[v][i] * q);
+                dr[v][i] += q * (b[i] * dx[v][i] - r[v][i] * m);
             }
-            if (a.gate_kind == kGateFull && a.d_gate) store8<ACT>(a.d_gate, at + c, t);
+            store8<RES>(a.d_resid, at + c, dr[v]);
+            if (!a.y) continue;
+            float g[8], dg[8];
+            if (KIND == kGateFull) load8<ACT>(a.gate, at + c, g);
+            float own_w[8];
+            if constexpr (!kHold) weight(v, own_w);
+            const float(&w)[8] = kHold ? held_w[kHold ? v : 0] : own_w;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {   // from here on y: n, dr: w d r, and k with a full gate
+                y[v][i] *= p;
+                const float e = dr[v][i] * y[v][i];
+                dr[v][i] *= w[i];
+                if constexpr (KIND == kGateFull) {
+                    dg[i] = dr[v][i] * y[v][i];
+                    s_q[v][i] += g[i] * e;
+                    dr[v][i] *= g[i];
+                } else {
+                    s_q[v][i] += tok * e;
+                }
+                kn[0] += dr[v][i] * y[v][i];
+            }
+            if (KIND == kGateFull && a.d_gate) store8<ACT>(a.d_gate, at + c, dg);
         }
-        if (a.y) {
-            row_sums<2, WAVES>(rs, red[2][sub], wave);
-            const float mk = post ? rs[0] * inv_h : 0.0f;
+        if (!a.y) continue;
+        if (post || KIND == kGateToken) row_sums<1, WAVES>(kn, red[2][sub], wave);
+        const float mk = post ? kn[0] * inv_h : 0.0f, out = p * tok;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                if (!in[v]) continue;
+        for (int v = 0; v < V; ++v) {
+            if (!in[v]) continue;
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = out * (dr[v][i] - y[v][i] * mk);
+            store8<ACT>(a.d_y, at + c0 + v * WAVES * 512, t);
+        }
+        if (KIND == kGateToken && a.d_gate && live && wave == 0 && (threadIdx.x & 63) == 0) static_cast<float *>(a.d_gate)[row] = kn[0];
+    }
+    // Q times scale and the gate is d post_gain, times scale and post_gain the gate's
+    const bool want[3] = {a.d_pre_gain != nullptr, a.d_post_gain != nullptr, KIND == kGateChannel && a.gate && a.d_gate};
+    if (ROWS > 1 && (want[0] || want[1] || want[2])) {   // the workgroup's rows side by side: theirs first become one
+        __shared__ float side[ROWS > 1 ? ROWS - 1 : 1][WAVES * 512];
+        static_assert(ROWS == 1 || V == 1, "one chunk a lane");
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float (&sum)[8] = k == 0 ? s_pre[0] : s_q[0];
+            __syncthreads();
+            if (sub > 0) store8<kF32>(side[sub - 1], c0, sum);
+            __syncthreads();
+            if (sub > 0) continue;
+#pragma unroll
+            for (int o = 0; o < ROWS - 1; ++o) {
                 float t[8];
+                load8<kF32>(side[o], c0, t);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) t[i] = p * (dx[v][i] - r[v][i] * mk);
-                store8<ACT>(a.d_y, at + c0 + v * WAVES * 512, t);
+                for (int i = 0; i < 8; ++i) sum[i] += t[i];
             }
-            if (a.gate_kind == kGateToken && a.d_gate && live && wave == 0 && (threadIdx.x & 63) == 0)
-                static_cast<float *>(a.d_gate)[row] = rs[1];
         }
     }
+    if (sub > 0) return;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int c = c0 + v * WAVES * 512;
         if (c >= a.H) continue;
-        const size_t plane = (size_t)slices * a.H, o = (size_t)slice * a.H + c;
-        if (a.d_pre_gain) store8<kF32>(a.parts, o, s_pre[v]);
-        if (a.d_post_gain) store8<kF32>(a.parts, plane + o, s_post[v]);
-        if (a.gate_kind == kGateChannel && a.d_gate) store8<kF32>(a.parts, 2 * plane + o, s_gate[v]);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            if (!want[k]) continue;
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = 1.0f;
+            if (k == 1 && KIND == kGateChannel && a.gate) load8<ACT>(a.gate, c, t);
+            if (k == 2 && a.post_gain) load8<ACT>(a.post_gain, c, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) t[i] = k == 0 ? s_pre[v][i] : a.scale * t[i] * s_q[v][i];
+            store8<kF32>(a.parts, ((size_t)k * gridDim.x + blockIdx.x) * a.H + c, t);
+        }
     }
 }
 
-// out[c] = sum over the slices, 32 columns a workgroup: 8 threads of 4 columns
-// by 32 runs of slices, the runs then added in order.
-__global__ __launch_bounds__(256) void k_norm_parts(const float *parts, int slices, int H, float *d_pre, float *d_post,
+// out[c] = sum over the slices, 32 columns a workgroup: 8 threads of 4 columns by
+// 64 runs of slices, 16 loads of each in flight; the runs are then added in order,
+// eight by eight.
+__global__ __launch_bounds__(512) void k_norm_parts(const float *parts, int slices, int H, float *d_pre, float *d_post,
                                                     float *d_gate) {
-    __shared__ f32x4_t sh[32][8];
+    __shared__ f32x4_t sh[64][8];
     float *out = blockIdx.y == 0 ? d_pre : blockIdx.y == 1 ? d_post : d_gate;
     if (!out) return;
     const int q = threadIdx.x & 7, run = threadIdx.x >> 3;
@@ -308,13 +373,22 @@ __global__ __launch_bounds__(256) void k_norm_parts(const float *parts, int slic
     f32x4_t s = {0.0f, 0.0f, 0.0f, 0.0f};
     if (c < H) {
         const float *p = parts + (size_t)blockIdx.y * slices * H + c;
-#pragma unroll 8
-        for (int i = run; i < slices; i += 32) s += *reinterpret_cast<const f32x4_t *>(p + (size_t)i * H);
+#pragma unroll 16
+        for (int i = run; i < slices; i += 64) s += *reinterpret_cast<const f32x4_t *>(p + (size_t)i * H);
     }
     sh[run][q] = s;
     __syncthreads();
+    if (run < 8) {
+        s = sh[8 * run][q];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += sh[8 * run + i][q];
+    }
+    __syncthreads();
+    if (run < 8) sh[run][q] = s;
+    __syncthreads();
     if (run == 0 && c < H) {
-        for (int i = 1; i < 32; ++i) s += sh[i][q];
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += sh[i][q];
         *reinterpret_cast<f32x4_t *>(out + c) = s;
     }
 }
@@ -349,29 +423,32 @@ void launch_norm_residual(const NormArgs &a, int act, int res, hipStream_t s) {
     });
 }
 
-// Workgroups of the backward pass, and partial rows that they leave.
-static int back_groups(int64_t T, int H, int rows) {
-    const int64_t want = (T + rows - 1) / rows;
-    const int64_t most = H <= 2048 ? 1024 / rows : H <= 4096 ? 512 : 256;
+// Workgroups of the backward pass, each of which leaves one partial row: 16 waves
+// a CU, which the registers allow.
+int norm_back_slices(int64_t T, int H) {
+    const int rows = H <= 512 ? 4 : H <= 1024 ? 2 : 1;   // side by side in a workgroup
+    const int64_t want = (T + rows - 1) / rows, most = H <= 2048 ? 1024 : H <= 4096 ? 512 : 256;
     return (int)(want < most ? want : most);
 }
-static int back_rows(int H) { return H <= 512 ? 4 : H <= 1024 ? 2 : 1; }
-
-int norm_back_slices(int64_t T, int H) { return back_groups(T, H, back_rows(H)) * back_rows(H); }
 
 void launch_norm_residual_backward(const NormBackArgs &a, int act, int res, hipStream_t s) {
     const int slices = norm_back_slices(a.T, a.H);
     if (a.T > 0) {
         by_types(act, res, [&](auto A, auto R) {
             by_width<A(), R()>(a.H, [&](auto W, auto V, auto N) {
-                hipLaunchKernelGGL((k_norm_back<A(), R(), W(), V(), N()>), dim3(slices / N()), dim3(64 * W() * N()), 0, s, a);
+                if (a.gate_kind == kGateToken)
+                    hipLaunchKernelGGL((k_norm_back<A(), R(), W(), V(), N(), kGateToken>), dim3(slices), dim3(64 * W() * N()), 0, s, a);
+                else if (a.gate_kind == kGateFull)
+                    hipLaunchKernelGGL((k_norm_back<A(), R(), W(), V(), N(), kGateFull>), dim3(slices), dim3(64 * W() * N()), 0, s, a);
+                else
+                    hipLaunchKernelGGL((k_norm_back<A(), R(), W(), V(), N(), kGateChannel>), dim3(slices), dim3(64 * W() * N()), 0, s, a);
             });
         });
         if (hipPeekAtLastError() != hipSuccess) return;
     }
     float *gate = a.gate_kind == kGateChannel ? static_cast<float *>(a.d_gate) : nullptr;
     if (a.d_pre_gain || a.d_post_gain || gate)
-        hipLaunchKernelGGL(k_norm_parts, dim3((a.H + 31) / 32, 3), dim3(256), 0, s, a.parts, slices, a.H, a.d_pre_gain,
+        hipLaunchKernelGGL(k_norm_parts, dim3((a.H + 31) / 32, 3), dim3(512), 0, s, a.parts, slices, a.H, a.d_pre_gain,
                            a.d_post_gain, gate);
 }
 
