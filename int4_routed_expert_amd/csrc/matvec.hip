@@ -31,6 +31,9 @@ namespace moe_w4 {
 struct MatvecPlan {
     int cols;       // columns of x
     int tiles;      // 16-row tiles
+    int run;        // tiles of a workgroup, one more in the first `more`
+    int more;
+    uint32_t inv;   // ceil(2^32 / blocks of a row)
 };
 
 namespace {
@@ -43,6 +46,18 @@ constexpr int kLdsBytes = 160 * 1024;
 __device__ __forceinline__ f32x4_t mfma16(uint4 a, uint4 b, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
                                                    0, 0, 0);
+}
+
+__device__ __forceinline__ uint2 bload8(__amdgpu_buffer_rsrc_t r, uint32_t voff) {
+    const auto v = __builtin_amdgcn_raw_buffer_load_b64(r, voff, 0, 0);
+    return make_uint2(v[0], v[1]);
+}
+
+// Lanes 8..15 of every 16 of a change places with lanes 0..7 of b.
+__device__ __forceinline__ void swap_halves(uint32_t &a, uint32_t &b) {
+    const uint32_t c = __builtin_amdgcn_update_dpp(a, b, 0x128, 0xf, 0xc, false);
+    b = __builtin_amdgcn_update_dpp(b, a, 0x128, 0xf, 0x3, false);
+    a = c;
 }
 
 // Eight codes -> eight bf16 values 24 + c in the order 0 4 1 5 2 6 3 7.
@@ -113,7 +128,9 @@ __device__ __forceinline__ void make_operands(const MatvecArgs &a, int cols, int
                     }
 #pragma unroll
                     for (int d = 1; d < GROUP / 8; d <<= 1) sum += shfl_xor_f(sum, d);
-                    xs[place * cols + col + p] =
+                    // (one group a block: codes as a lane loads them, its 32 in the four MFMAs)
+                    const int to = GROUP == 128 ? (place & ~15) | (j & 3) << 2 | j >> 2 : place;
+                    xs[to * cols + col + p] =
                         make_uint4(b[0] | (b[4] << 16), b[1] | (b[5] << 16), b[2] | (b[6] << 16), b[3] | (b[7] << 16));
                     if (j % (GROUP / 8) == 0) starts[(blk * kGroups + j / (GROUP / 8)) * (16 * CT) + col + p] = -24.0f * sum;
                 }
@@ -161,9 +178,14 @@ __global__ __launch_bounds__(64 * waves_of(CT), simd_waves(CT)) void k_matvec(Ma
     const float *startsw = reinterpret_cast<const float *>(xw + (size_t)blocks * 16 * cols);
 
     // tiles [tile0, tile1) of this workgroup; of their blocks in a row this wave's [begin, end)
-    const int tile0 = (int)((int64_t)plan.tiles * blockIdx.x / gridDim.x), tile1 = (int)((int64_t)plan.tiles * (blockIdx.x + 1) / gridDim.x);
-    const int all = (tile1 - tile0) * blocks;
-    auto part = [&](int w) { return (int)((int64_t)all * w / kWaves); };
+    const int block0 = (int)blockIdx.x, tile0 = block0 * plan.run + min(block0, plan.more);
+    const int all = (plan.run + (block0 < plan.more)) * blocks;
+    // at / blocks, at <= 2^21 (at most 2^12 tiles of 2^9 blocks), by a product
+    auto tile_of = [&](int at) { return blocks == 1 ? at : (int)__umulhi((uint32_t)at, plan.inv); };
+    auto part = [&](int w) {   // from even blocks of a tile on
+        const int at = (int)((uint32_t)(all * w) / kWaves);
+        return at - ((at - tile_of(at) * blocks) & 1);
+    };
     const int begin = __builtin_amdgcn_readfirstlane(part(wave)), end = __builtin_amdgcn_readfirstlane(part(wave + 1));
 
     // A batch: n blocks from block b of a tile.
@@ -177,32 +199,43 @@ __global__ __launch_bounds__(64 * waves_of(CT), simd_waves(CT)) void k_matvec(Ma
         if (p.b == blocks) p.b = 0, ++p.tile;
         fill(p);
     };
+    // Scales come for kWindow batches at a time, those of batch i of a window in the
+    // lanes of g = i; the other batches' loads are out of range, which keeps the
+    // count of loads the same for every batch.  Rows of group size 128 with an odd
+    // number of blocks are only aligned to 2 bytes: the second scale is loaded apart.
+    constexpr int kWords = kBatch * kGroups / 2, kWindow = 4;
+    const bool even = !(blocks & 1);
     struct Batch {
         uint4 codes[kBatch];
-        uint32_t scales[kBatch][GROUP == 32 ? 2 : 1];
+        uint32_t scales[kWords], odd;
     };
-    // a lane's byte in its 16 rows; rows behind the last are out of the buffers' range and read as zeros
+    // A batch's codes are 128 bytes of each of 16 rows, loaded as whole lines of 8 rows
+    // at a time (loads alone, one token, 150144 x 2048: 29 us, and 34 with 64 bytes of 16
+    // rows); swap_halves gives each lane its row's.
+    // Rows behind the last are out of the buffers' range and read as zeros.
     const uint32_t code_pitch = (uint32_t)a.k / 2, scale_pitch = (uint32_t)a.k / GROUP * 2;
-    const uint32_t code_at = t * code_pitch + 16 * g, scale_at = t * scale_pitch;
+    const uint32_t code_at = (t & 7) * code_pitch + 16 * (g + (t >> 3) * 4), scale_at = t * scale_pitch + g * (4 * kWords);
+    auto new_window = [&](const Place &p) { return p.b % (kBatch * kWindow) == 0 || p.left == end - begin; };
     auto load = [&](Batch &w, const Place &p) {
         const int64_t row = (int64_t)p.tile * 16;
-        const uint32_t left = (uint32_t)max(0, min(16, a.n - (int)row));
+        const uint32_t left = p.left > 0 ? (uint32_t)min(16, a.n - (int)row) : 0u;   // nothing is read behind the last
         const __amdgpu_buffer_rsrc_t codes = make_buf(a.codes + row * code_pitch, left * code_pitch);
         const __amdgpu_buffer_rsrc_t scales = make_buf(reinterpret_cast<const uint8_t *>(a.scales) + row * scale_pitch, left * scale_pitch);
-#pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            if (u >= p.n) break;
-            const uint32_t b = p.b + u;
-            w.codes[u] = bload16_nt(codes, code_at + b * 64, 0);
-            if constexpr (GROUP == 32) {
-                w.scales[u][0] = bload4(scales, scale_at + b * 8, 0);
-                w.scales[u][1] = bload4(scales, scale_at + b * 8 + 4, 0);
-            } else if constexpr (GROUP == 64) {
-                w.scales[u][0] = bload4(scales, scale_at + b * 4, 0);
-            } else {
-                w.scales[u][0] = bload2(scales, scale_at + b * 2, 0);
-            }
+        const uint32_t at = scale_at + p.b / (kBatch * kWindow) * (kWindow * 4 * kWords) + (new_window(p) ? 0u : 0x80000000u);
+        if constexpr (GROUP == 32) {
+            const uint4 q = bload16(scales, at, 0);
+            w.scales[0] = q.x, w.scales[1] = q.y, w.scales[2] = q.z, w.scales[3] = q.w;
+        } else if constexpr (GROUP == 64) {
+            const uint2 q = bload8(scales, at);
+            w.scales[0] = q.x, w.scales[1] = q.y;
+        } else if (even) {
+            w.scales[0] = bload4(scales, at, 0);
+        } else {
+            w.scales[0] = bload2(scales, at, 0);
+            w.odd = bload2(scales, at + 2, 0);
         }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) w.codes[u] = bload16_nt(codes, code_at + u * 8 * code_pitch + p.b * 64, 0);
     };
 
     constexpr bool kHeadLds = head_in_lds(CT);
@@ -210,15 +243,24 @@ __global__ __launch_bounds__(64 * waves_of(CT), simd_waves(CT)) void k_matvec(Ma
     f32x4_t sum[CT], head[kHeadLds ? 1 : CT];   // of the tile at hand; of the head
 #pragma unroll
     for (int c = 0; c < CT; ++c) sum[c] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    const bool has_head = begin < end && begin % blocks != 0;
+    const int first = tile_of(begin), begin_at = begin - first * blocks;   // tile and block where this wave begins
+    const bool has_head = begin < end && begin_at != 0;
+    // Operands of x that come through the caches are loaded before the next weights, as
+    // loads return in order (64 tokens, 12288 x 6144: 43 us, and 62 when they are loaded
+    // at the products; more column tiles have no registers for it)
+    constexpr bool kFetch = !LDS && CT <= 4;
+    uint4 ahead[kFetch ? kBatch : 1][kFetch ? CT : 1][kFetch ? 4 : 1];
+    uint32_t window[kWords], window_odd = 0, scales[kWords], odd = 0;
     auto block = [&](Batch &w, int u, int b) {
-        transpose4(w.codes[u]);
+        if constexpr (GROUP != 128) transpose4(w.codes[u]);
         const uint32_t wd[4] = {w.codes[u].x, w.codes[u].y, w.codes[u].z, w.codes[u].w};
         const int at = (b * 16 + g) * cols + (CT == 1 ? min(t, cols - 1) : t);
         const int st = b * kGroups * (16 * CT) + 4 * g;
 #pragma unroll
         for (int gr = 0; gr < kGroups; ++gr) {
-            const float s = (gr & 1) ? bf16hi(w.scales[u][gr >> 1]) : bf16lo(w.scales[u][gr >> 1]);
+            const int i = u * kGroups + gr;
+            float s = (i & 1) ? bf16hi(scales[i >> 1]) : bf16lo(scales[i >> 1]);
+            if (GROUP == 128 && u == 1 && !even) s = bf16lo(odd);
             uint4 q[kPer];
 #pragma unroll
             for (int k = 0; k < kPer; ++k) q[k] = codes_to_bf16(wd[gr * kPer + k]);
@@ -226,9 +268,24 @@ __global__ __launch_bounds__(64 * waves_of(CT), simd_waves(CT)) void k_matvec(Ma
             for (int c = 0; c < CT; ++c) {
                 f32x4_t acc = *reinterpret_cast<const f32x4_t *>((LDS ? starts : startsw) + st + (gr * CT + c) * 16);
 #pragma unroll
-                for (int k = 0; k < kPer; ++k) acc = mfma16((LDS ? xs : xw)[at + (gr * kPer + k) * 4 * cols + c * 16], q[k], acc);
+                for (int k = 0; k < kPer; ++k) {
+                    const int i = gr * kPer + k;
+                    acc = mfma16(kFetch ? ahead[kFetch ? u : 0][kFetch ? c : 0][kFetch ? i : 0]
+                                        : (LDS ? xs : xw)[at + i * 4 * cols + c * 16], q[k], acc);
+                }
                 sum[c] += s * acc;
             }
+        }
+    };
+    auto fetch = [&](const Place &p) {
+        if constexpr (kFetch) {
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int c = 0; c < CT; ++c)
+                        ahead[u][c][i] = xw[(min(p.b + u, blocks - 1) * 16 + g + 4 * i) * cols + (CT == 1 ? min(t, cols - 1) : t) + c * 16];
         }
     };
     auto store = [&](int tile) {   // element i of sum[c] is column 16 c + 4 g + i of row t
@@ -250,6 +307,21 @@ __global__ __launch_bounds__(64 * waves_of(CT), simd_waves(CT)) void k_matvec(Ma
             }
     };
     auto compute = [&](Batch &w, const Place &p) {
+        swap_halves(w.codes[0].x, w.codes[1].x);
+        swap_halves(w.codes[0].y, w.codes[1].y);
+        swap_halves(w.codes[0].z, w.codes[1].z);
+        swap_halves(w.codes[0].w, w.codes[1].w);
+        const bool fresh = new_window(p);
+        const int from = (t + 16 * (p.b / kBatch % kWindow)) * 4;
+#pragma unroll
+        for (int i = 0; i < kWords; ++i) {
+            window[i] = fresh ? w.scales[i] : window[i];
+            scales[i] = __builtin_amdgcn_ds_bpermute(from, window[i]);
+        }
+        if (GROUP == 128 && !even) {
+            window_odd = fresh ? w.odd : window_odd;
+            odd = __builtin_amdgcn_ds_bpermute(from, window_odd);
+        }
         if (p.n == kBatch) {   // no branch between the blocks: their loads and products overlap
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) block(w, u, p.b + u);
@@ -260,7 +332,7 @@ __global__ __launch_bounds__(64 * waves_of(CT), simd_waves(CT)) void k_matvec(Ma
         }
         if (p.b + p.n < blocks) return;
         // the tile's last block: it is whole, or (the first one) the head
-        const bool is_head = has_head && p.tile == tile0 + begin / blocks;
+        const bool is_head = has_head && p.tile == tile0 + first;
         if (!is_head) store(p.tile);
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
@@ -273,7 +345,7 @@ __global__ __launch_bounds__(64 * waves_of(CT), simd_waves(CT)) void k_matvec(Ma
     };
 
     // products one batch behind the loads
-    Place p{tile0 + begin / blocks, begin % blocks, 0, end - begin};
+    Place p{tile0 + first, begin_at, 0, end - begin};
     fill(p);
     Batch w0, w1;
     load(w0, p);
@@ -284,18 +356,21 @@ __global__ __launch_bounds__(64 * waves_of(CT), simd_waves(CT)) void k_matvec(Ma
     while (p.left > 0) {
         Place p1 = p;
         next(p1);
+        fetch(p);
         load(w1, p1);
         compute(w0, p);
         if (p1.left <= 0) break;
         p = p1;
         next(p);
+        fetch(p1);
         load(w0, p);
         compute(w1, p1);
     }
 
     // Tiles that several waves share: the wave with the first blocks adds the others' sums.
-    const bool middle = has_head && begin / blocks == (end - 1) / blocks && end % blocks != 0;   // neither end is this wave's
-    const bool has_tail = begin < end && end % blocks != 0 && !middle;
+    const int last = tile_of(max(end - 1, 0));
+    const bool middle = has_head && first == last && end != (last + 1) * blocks;   // neither end is this wave's
+    const bool has_tail = begin < end && end != (last + 1) * blocks && !middle;
     if (!kHeadLds) __syncthreads();   // the sums take the place of x
     if (has_head && (middle || !kHeadLds)) {
 #pragma unroll
@@ -303,13 +378,13 @@ __global__ __launch_bounds__(64 * waves_of(CT), simd_waves(CT)) void k_matvec(Ma
     }
     __syncthreads();
     if (has_tail) {
-        const int tile = (end - 1) / blocks, stop = (tile + 1) * blocks;
+        const int stop = (last + 1) * blocks;
         for (int w = wave + 1; w < kWaves && part(w) < stop; ++w) {
             if (part(w) == part(w + 1)) continue;   // no blocks
 #pragma unroll
             for (int c = 0; c < CT; ++c) sum[c] += red[(w * CT + c) * 64 + lane];
         }
-        store(tile0 + tile);
+        store(tile0 + last);
     }
 }
 
@@ -366,6 +441,9 @@ void launch_matvec(const MatvecArgs &a, hipStream_t s) {
     const int one = (p.tiles + 255) / 256, two = 2 * ((p.tiles + 511) / 512);
     const int slots = ct == 1 && kLdsBytes / lds >= 2 && (two <= one || one > 8) ? 512 : 256;
     const unsigned grid = (unsigned)(p.tiles < slots ? p.tiles : slots);
+    p.run = p.tiles / (int)grid;
+    p.more = p.tiles % (int)grid;
+    p.inv = (uint32_t)(((1ull << 32) + blocks - 1) / blocks);
     auto go = [&](auto G, auto C, auto P) {
         if (!in_lds) {
             hipLaunchKernelGGL((k_matvec_x<G(), C(), P()>), dim3((unsigned)((a.m * blocks + 15) / 16)), dim3(256), 0, s, a, p);
@@ -375,9 +453,11 @@ void launch_matvec(const MatvecArgs &a, hipStream_t s) {
             hipLaunchKernelGGL((k_matvec<G(), C(), P(), true>), dim3(grid), dim3(64 * waves), lds, s, a, p);
         }
     };
-    auto by_parts = [&](auto G, auto C) {
-        if (parts == 1) go(G, C, std::integral_constant<int, 1>{});
-        else if (parts == 2) go(G, C, std::integral_constant<int, 2>{});
+    auto by_parts = [&](auto G, auto C) {   // (eight column tiles: only two and three parts need so many)
+        if constexpr (C() < 8) {
+            if (parts == 1) return go(G, C, std::integral_constant<int, 1>{});
+        }
+        if (parts == 2) go(G, C, std::integral_constant<int, 2>{});
         else go(G, C, std::integral_constant<int, 3>{});
     };
     auto by_tiles = [&](auto G) {
