@@ -201,10 +201,11 @@ __global__ __launch_bounds__(64 * waves_of(CT), simd_waves(CT)) void k_matvec(Ma
     };
     // Scales come for kWindow batches at a time, those of batch i of a window in the
     // lanes of g = i; the other batches' loads are out of range, which keeps the
-    // count of loads the same for every batch.  Rows of group size 128 with an odd
-    // number of blocks are only aligned to 2 bytes: the second scale is loaded apart.
+    // count of loads the same for every batch.  Group size 128: where rows of an odd
+    // number of blocks or the tensor's start are aligned to 2 bytes only, the second
+    // scale of a batch is loaded apart.
     constexpr int kWords = kBatch * kGroups / 2, kWindow = 4;
-    const bool even = !(blocks & 1);
+    const bool even = !(blocks & 1) && (reinterpret_cast<uintptr_t>(a.scales) & 3) == 0;
     struct Batch {
         uint4 codes[kBatch];
         uint32_t scales[kWords], odd;

@@ -402,10 +402,11 @@ def moe_w4_grouped_mm_dw(x, dy, offsets, dw, add=None, workspace=None, stream=No
     room = 0
     if workspace is None:
         room = _lib.moe_w4_grouped_mm_dw_workspace_bytes(e, m, n, k)
-        if room:
+        if room and stream is None:
             workspace = torch.empty((room,), dtype=_u8, device=x.device)
-            if stream is not None:   # the allocator must know of a stream other than the current one
-                workspace.record_stream(torch.cuda.ExternalStream(stream, x.device) if isinstance(stream, int) else stream)
+        elif room:   # memory of the call's own stream: what the current one last used may still be in use there
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream, x.device) if isinstance(stream, int) else stream):
+                workspace = torch.empty((room,), dtype=_u8, device=x.device)
     else:
         (room,), _ = _other(name, "workspace", workspace, 1, (_u8,))
     _enqueue(name, _lib.moe_w4_grouped_mm_dw, gpu, stream, (
