@@ -7,11 +7,12 @@
 //
 // One tile kernel serves the three: out[m][c] = sum_l A(m, l) B(c, l), where an
 // operand is either "K-major" (l contiguous in memory: x and w of mm, dy of
-// dx) or "MN-major" (its m or c contiguous, one row per l: w of dx, dy and x
-// of dw).  l advances kStep = 64 a step.  Both kinds go from global memory to
-// LDS with 16-byte buffer loads that bypass the registers, STAGES steps ahead; a K-major fragment of v_mfma_f32_16x16x32 is one 16-byte LDS read, an
-// MN-major one two transposing 8-byte LDS reads (ds_read_b64_tr_b16: in each
-// group of 16 lanes, lane t receives element t of 4 rows of 16 elements).
+// dx) or "MN-major" (its m or c contiguous, one row per l: w of dx, dy and x of
+// dw).  l advances kStep = 64 a step.  Both kinds go from global memory to LDS
+// with 16-byte buffer loads that bypass the registers, STAGES steps ahead; a
+// K-major fragment of v_mfma_f32_16x16x32 is one 16-byte LDS read, an MN-major one
+// two transposing 8-byte LDS reads (ds_read_b64_tr_b16: in each group of 16 lanes,
+// lane t receives element t of 4 rows of 16 elements).
 //
 // Workgroups are as many as the chip holds, and each walks its share of the tiles
 // as one stream of steps: the loads run ahead across the borders of the tiles,
@@ -26,6 +27,13 @@
 // extent aim past every descriptor; the hardware's range check makes both
 // zeros in LDS.  Descriptors of MN-major operands move with l, so offsets
 // stay small whatever the tensors' sizes are.
+//
+// Measured (MI355X): 256 experts, 1024 x 2048, bf16: 192 rows 99 us (5.7 TB/s, the
+// weights' stream), 12288 uneven rows 218 us (5.3 TB/s), 393216 rows 1529 us (1079
+// TFLOP/s: a large library product reaches 1478); dw of 98304 rows into fp32, added
+// to, 1094 us (4.5 TB/s, a copy reaches 4.9); dx of 20011 fp16 rows of 60 experts,
+// 1400 x 2056, 184 us (626 TFLOP/s: the ninth column tile holds 8 columns, and 1080
+// tiles are five rounds of the CUs where 4.2 would do).
 #include <type_traits>
 
 #include "common.h"
