@@ -424,11 +424,15 @@ static bool x_fits(const MatvecArgs &a, int m, int parts) {
 void launch_matvec(const MatvecArgs &a, hipStream_t s) {
     const int parts = x_parts(a), ct = column_tiles(a.m, parts);
     const bool in_lds = x_fits(a, a.m, parts);
-    // Operands that do not fit LDS, but do in two halves, and many rows to read them
-    // for: the weights are read twice (64 tokens, 150144 x 2048: 107 us against 186 with
-    // x read through the caches; 16 tokens, 2048 x 6144: 27 us against 10)
+    // In two halves, which read the weights twice:
+    //   sixteen column tiles, and eight of group size 32 without LDS: their sums would
+    //   spill (64 rotated tokens to fp32, 12288 x 2048: 54 us against 127; 64 rotated
+    //   fp16 tokens, 2048 x 2048, group size 32: 23 against 37, but 128: 41 against 29);
+    //   operands that only fit LDS so, and many rows to read them for (64 tokens,
+    //   150144 x 2048: 92 us against 186 with x read through the caches; 16 tokens, 2048
+    //   x 6144: 27 us against 10)
     const int half = (a.m + 1) / 2;
-    if (!in_lds && a.n >= 32768 && x_fits(a, half, parts)) {
+    if (ct == 16 || (!in_lds && ((ct == 8 && a.group == 32) || (a.n >= 32768 && x_fits(a, half, parts))))) {
         MatvecArgs h = a;
         h.m = half;
         launch_matvec(h, s);
@@ -452,13 +456,15 @@ void launch_matvec(const MatvecArgs &a, hipStream_t s) {
     p.more = p.tiles % (int)grid;
     p.inv = (uint32_t)(((1ull << 32) + blocks - 1) / blocks);
     auto go = [&](auto G, auto C, auto P) {
-        if (!in_lds) {
-            hipLaunchKernelGGL((k_matvec_x<G(), C(), P()>), dim3((unsigned)((a.m * blocks + 15) / 16)), dim3(256), 0, s, a, p);
-            if (hipPeekAtLastError() != hipSuccess) return;
-            hipLaunchKernelGGL((k_matvec<G(), C(), P(), false>), dim3(grid), dim3(64 * waves), lds, s, a, p);
-        } else {
-            hipLaunchKernelGGL((k_matvec<G(), C(), P(), true>), dim3(grid), dim3(64 * waves), lds, s, a, p);
+        if constexpr (C() < 8 || G() > 32) {
+            if (!in_lds) {
+                hipLaunchKernelGGL((k_matvec_x<G(), C(), P()>), dim3((unsigned)((a.m * blocks + 15) / 16)), dim3(256), 0, s, a, p);
+                if (hipPeekAtLastError() != hipSuccess) return;
+                hipLaunchKernelGGL((k_matvec<G(), C(), P(), false>), dim3(grid), dim3(64 * waves), lds, s, a, p);
+                return;
+            }
         }
+        hipLaunchKernelGGL((k_matvec<G(), C(), P(), true>), dim3(grid), dim3(64 * waves), lds, s, a, p);
     };
     auto by_parts = [&](auto G, auto C) {   // (eight column tiles: only two and three parts need so many)
         if constexpr (C() < 8) {
@@ -471,8 +477,7 @@ void launch_matvec(const MatvecArgs &a, hipStream_t s) {
         if (ct == 1) by_parts(G, std::integral_constant<int, 1>{});
         else if (ct == 2) by_parts(G, std::integral_constant<int, 2>{});
         else if (ct == 4) by_parts(G, std::integral_constant<int, 4>{});
-        else if (ct == 8) by_parts(G, std::integral_constant<int, 8>{});
-        else go(G, std::integral_constant<int, 16>{}, std::integral_constant<int, 3>{});   // (only three parts need so many)
+        else by_parts(G, std::integral_constant<int, 8>{});
     };
     if (a.group == 32) by_tiles(std::integral_constant<int, 32>{});
     else if (a.group == 64) by_tiles(std::integral_constant<int, 64>{});
