@@ -98,7 +98,7 @@ def test_norm(m):
 
 def test_norm_backward(m):
     nb = m.moe_w4_norm_workspace_bytes(4, 64)
-    assert nb >= 3 * 4 * 64 * 4 and m.moe_w4_norm_workspace_bytes(4, 60) == 0 and m.moe_w4_norm_workspace_bytes(-1, 64) == 0
+    assert nb >= 3 * 64 * 4 and m.moe_w4_norm_workspace_bytes(4, 60) == 0 and m.moe_w4_norm_workspace_bytes(-1, 64) == 0
 
     def call(r=X, y=W, gate=None, kind=0, scale=1.0, post=None, pre=None, flags=2, eps=1e-6, T=4, H=64, dt=m.BF16, rt=m.F32, up=0x60000000,
              dx=0x61000000, dr=0x62000000, dy=0x63000000, dg=None, da=None, db=None, ws=WS, nb=nb):
