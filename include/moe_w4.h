@@ -417,7 +417,8 @@ size_t moe_w4_grouped_mm_dw_workspace_bytes(int64_t n_groups, int64_t M, int64_t
  * moe_w4_matvec_workspace_bytes(M, K) bytes, contents on entry irrelevant.
  * Pointers 16-byte aligned (scales 256 / group); y overlaps no input and not
  * the workspace.  A token whose x is not finite has results that are not
- * finite.  EINVAL / EWORKSPACE otherwise. */
+ * finite, and so may one for which 32 times a group's sum of |xr| is not (sums
+ * hold the codes with 24 added).  EINVAL / EWORKSPACE otherwise. */
 #define MOE_W4_MATVEC_MAX_TOKENS 64
 #define MOE_W4_MATVEC_MAX_K 65536
 #define MOE_W4_MATVEC_MAX_N 16777216

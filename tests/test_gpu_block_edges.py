@@ -143,6 +143,18 @@ def test_scales_aligned_to_two_bytes(m, k):
     assert ((y.double() - x.double() @ w.T).abs() <= bar(x, s, 128)).all()
 
 
+@pytest.mark.parametrize("tokens,k,group", [(1, 384, 128), (3, 640, 64), (20, 384, 32), (2, 128, 128), (40, 1664, 128), (1, 6272, 32)])
+def test_runs_of_tiles_with_odd_blocks(m, tokens, k, group):
+    """Several tiles of 16 rows a workgroup, whose waves' shares begin and end inside tiles of an odd number of blocks."""
+    n, g = 12007, torch.Generator().manual_seed(6)
+    codes = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, generator=g).cuda()
+    scales = (torch.rand((n, k // group), generator=g) + 0.5).bfloat16().cuda()
+    x, y = normal(tokens, k), torch.empty((tokens, n), device="cuda")
+    m.moe_w4_matvec(x, codes, scales, y, m.matvec_workspace(tokens, k))
+    w, s = weights(codes, scales, group)
+    assert ((y.double() - x.double() @ w.T).abs() <= bar(x, s, group)).all()
+
+
 def test_dw_takes_its_workspace_from_the_calls_stream(m, monkeypatch):
     n = k = 64
     x, dy = normal(40000, k), normal(40000, n, seed=2)
