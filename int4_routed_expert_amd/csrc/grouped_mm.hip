@@ -579,16 +579,22 @@ static void launch_tile(const GroupedArgs &g, hipStream_t s) {
 //   256 x 12288 x 1024 x 2048    260      223     221    296     (uneven groups) weights bound it: little work on absent rows
 //   256 x   192 x 1024 x 2048    136      116     101    100
 //     1 x  4096 x 2048 x 2048     52       37      50    114     too few large tiles for the CUs
+//     8 x  7168 x 2048 x 2048    102       75                    264 large tiles: a second round of the CUs for 8
+//     8 x 14336 x 2048 x 2048    106      133                    488 large tiles: two full rounds
+//    16 x 12288 x 1152 x 2048 dx  98       66                    285 large tiles
 //     8 x   256 x 2048 x 2048     31       23      22     19     latency: the most, smallest tiles
 constexpr int kMinRows = 80, kFewRows = 16;        // rows a group
-constexpr int kMinTiles256 = 160, kFewTiles128 = 128;
+constexpr int kFewTiles128 = 128;
+// Large tiles go in whole rounds of the CUs; small ones, two a CU, so evenly that a
+// part of a round counts as a part, and 512 of them take 0.8 of a large round.
+constexpr int kSmallPerRound = 640;
 
 template <int MODE, bool BF16>
 static void launch_rows(const GroupedArgs &g, hipStream_t s) {
     const int C = MODE == kMm ? g.n : g.k;
     const int held = min(g.groups, g.rows), per = g.rows / held;
     auto tiles = [&](int bm, int bn) { return ((int64_t)g.rows / bm + held / 2 + 1) * ((C + bn - 1) / bn); };
-    if (per >= kMinRows && tiles(256, 256) >= kMinTiles256)
+    if (per >= kMinRows && tiles(128, 128) >= (tiles(256, 256) + kCus - 1) / kCus * kSmallPerRound)
         launch_tile<MODE, BF16, false, 256, 256, 2, 4, 2>(g, s);
     else if (MODE == kMm && (per <= kFewRows || tiles(128, 128) <= kFewTiles128))
         launch_tile<kMm, BF16, false, 32, 64, 2, 2, 4>(g, s);   // (dx of few rows: 117 us against 110 at 256 x 192 rows)

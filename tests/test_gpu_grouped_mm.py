@@ -81,9 +81,9 @@ def test_three_products(m, counts, n, k, dtype):
 
 # sizes whose tiles are the largest ones of each product (many rows a group and many tiles), the ones between, and
 # the smallest, each with ragged edges in every direction
-@pytest.mark.parametrize("which,groups,each,n,k", [("mm", 20, 300, 2056, 264), ("mm", 4, 700, 1032, 136), ("mm", 6, 200, 264, 72),
+@pytest.mark.parametrize("which,groups,each,n,k", [("mm", 8, 760, 2056, 264), ("mm", 20, 300, 2056, 264), ("mm", 4, 700, 1032, 136), ("mm", 6, 200, 264, 72),
                                                    ("mm", 40, 60, 648, 200), ("mm", 70, 3, 520, 264),
-                                                   ("dx", 20, 300, 264, 2056), ("dx", 4, 700, 136, 1032), ("dx", 40, 60, 200, 648),
+                                                   ("dx", 8, 760, 264, 2056), ("dx", 20, 300, 264, 2056), ("dx", 4, 700, 136, 1032), ("dx", 40, 60, 200, 648),
                                                    ("dw", 60, 90, 1400, 2056), ("dw", 5, 400, 1288, 520)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_tile_forms(m, which, groups, each, n, k, dtype):
